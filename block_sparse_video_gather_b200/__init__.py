@@ -30,7 +30,11 @@ SYMBOLS = (
     "vsa_coarse_compress", "vsa_untile_gate", "vsa_tile_coarse", "vsa_tile_coarse_static",
     "vsa_sparse_attn_bwd_workspace", "vsa_sparse_attn_bwd", "vsa_quantize_nvfp4", "vsa_sparse_attn_fwd_nvfp4",
     "vsa_coarse_topk_prefix", "vsa_tile_coarse_prefix", "vsa_sparse_attn_fwd_ws", "vsa_sparse_attn_fwd_nvfp4_ws",
+    "vsa_cache_page_bytes", "vsa_cache_tables", "vsa_cache_release", "vsa_cache_append_nvfp4", "vsa_cache_read_nvfp4",
+    "vsa_cache_attn_workspace", "vsa_cache_attn_nvfp4", "vsa_untile_merge",
 )
+
+CACHE_RECORD_BYTES = 2304  # 16 tokens of one head in the 4-bit key/value cache
 
 VSA_BF16 = 0
 VSA_F16 = 1
@@ -43,6 +47,7 @@ VSA_ERR_CUDA = 4
 VSA_ERR_BAD_INDEX = 5
 VSA_ERR_TIMEOUT = 6
 VSA_ERR_NO_DEVICE = 7
+VSA_ERR_CAPACITY = 8
 
 _lib = None
 
@@ -87,6 +92,15 @@ def lib():
         L.vsa_quantize_nvfp4.argtypes = [P, i, P, i, i, i, P, P, P]
         L.vsa_sparse_attn_fwd_nvfp4.argtypes = [P, i, P, P, P, P, P, P, P, i, i, i, i, P, P, P]
         L.vsa_sparse_attn_fwd_nvfp4_ws.argtypes = [P, i, P, P, P, P, P, P, P, i, i, i, i, P, P, P, P]
+        i64 = ctypes.c_int64
+        L.vsa_cache_page_bytes.argtypes = [i, i, i, P]
+        L.vsa_cache_tables.argtypes = [P, P, i, i, P, i, P, P, i, P, P, P, i, P, P]
+        L.vsa_cache_release.argtypes = [P, i, i, P, P, i, P, i, P, P]
+        L.vsa_cache_append_nvfp4.argtypes = [i, P, P, i64, i64, P, i, i, i, P, i, i, P]
+        L.vsa_cache_read_nvfp4.argtypes = [i, P, i, i, i, P, i, i, P, P, P]
+        L.vsa_cache_attn_workspace.argtypes = [i, i, i, P]
+        L.vsa_cache_attn_nvfp4.argtypes = [i, P, i64, P, P, i, i, i, i, i, i, P, i, i, P, i, i, P, P, P, P]
+        L.vsa_untile_merge.argtypes = [P, i, P, P, P, P, i, i, i, P, P, P]
         L.vsa_get_status.argtypes = [P, P]
         L.vsa_strerror.argtypes = [i]
         L.vsa_strerror.restype = ctypes.c_char_p
@@ -465,6 +479,185 @@ def sparse_attn_bwd(plan: Plan, q, k, v, o, lse, do, q2k_idx, q2k_num, dq=None, 
     return dq, dk, dv
 
 
+def _rows(t, what):
+    """A [T, heads, 128] tensor whose tokens may be strided (a slice of a fused projection):
+    (pointer, elements from token to token)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[2] != 128:
+        raise ValueError(f"{what} must be [tokens, heads, 128], got {tuple(t.shape)}")
+    T, H, D = t.shape
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != D):
+        raise ValueError(f"{what}: heads and channels must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (st[0] if T > 1 else max(st[0], H * D) & ~7)
+
+
+def _pages_shape(pages):
+    """(num_pages, Hkv, page_tokens) of a cache's pages [num_pages, Hkv, page_tokens / 16, 2304]."""
+    if pages.dim() != 4 or pages.shape[3] != CACHE_RECORD_BYTES:
+        raise ValueError(f"pages must be [num_pages, Hkv, page_tokens / 16, {CACHE_RECORD_BYTES}], got "
+                         f"{tuple(pages.shape)}")
+    return pages.shape[0], pages.shape[1], pages.shape[2] * 16
+
+
+def cache_pages(num_pages: int, Hkv: int, page_tokens: int = 64, device="cuda", D: int = 128):
+    """Pages of a 4-bit key/value cache (uninitialised): uint8 [num_pages, Hkv, page_tokens / 16, 2304]."""
+    n = ctypes.c_size_t(0)
+    _check(lib().vsa_cache_page_bytes(Hkv, D, page_tokens, ctypes.byref(n)), "vsa_cache_page_bytes")
+    return _torch().empty((num_pages, Hkv, page_tokens // 16, CACHE_RECORD_BYTES), dtype=_torch().uint8,
+                          device=device)
+
+
+def cache_tables(kv_len, new_len, page_tokens: int, free_pages, free_start, block_table, slots, kv_len_out=None,
+                 cu_out=None, free_next_out=None):
+    """Room for new_len[r] more tokens of every request: writes the new pages' entries of block_table
+    [R, max_pages] and the new tokens' slots (all of `slots`; -1 past the last), and returns (kv_len_out [R],
+    cu [R + 1], free_next [1]).  See vsa_cache_tables; kv_len_out and free_next must be other tensors than kv_len
+    and free_start."""
+    torch = _torch()
+    i32 = torch.int32
+    R = kv_len.shape[0]
+    if kv_len.shape != (R,) or new_len.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("kv_len and new_len must be [R], block_table [R, max_pages]")
+    if kv_len_out is None:
+        kv_len_out = torch.empty_like(kv_len)
+    if cu_out is None:
+        cu_out = torch.empty(R + 1, dtype=i32, device=kv_len.device)
+    if free_next_out is None:
+        free_next_out = torch.empty_like(free_start)
+    if kv_len_out.numel() != R or cu_out.numel() != R + 1 or free_next_out.numel() < 1 or free_start.numel() < 1:
+        raise ValueError("kv_len_out must hold R, cu_out R + 1, free_start and free_next_out 1 entries")
+    _check(lib().vsa_cache_tables(
+        _ptr(kv_len, i32, "kv_len"), _ptr(new_len, i32, "new_len"), R, page_tokens,
+        _ptr(free_pages, i32, "free_pages"), free_pages.numel(), _ptr(free_start, i32, "free_start"),
+        _ptr(block_table, i32, "block_table"), block_table.shape[1], _ptr(kv_len_out, i32, "kv_len_out"),
+        _ptr(cu_out, i32, "cu_out"), _ptr(slots, i32, "slots"), slots.numel(),
+        _ptr(free_next_out, i32, "free_next_out"), _stream()), "vsa_cache_tables")
+    return kv_len_out, cu_out, free_next_out
+
+
+def cache_release(drop, page_tokens: int, kv_len, block_table, free_pages, free_start):
+    """Gives the pages of the requests with drop[r] != 0 back to the stack and sets their kv_len to 0, in place."""
+    i32 = _torch().int32
+    R = kv_len.shape[0]
+    if drop.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("drop and kv_len must be [R], block_table [R, max_pages]")
+    d = drop.view(_torch().uint8) if drop.dtype == _torch().bool else drop
+    _check(lib().vsa_cache_release(
+        _ptr(d, _torch().uint8, "drop"), R, page_tokens, _ptr(kv_len, i32, "kv_len"),
+        _ptr(block_table, i32, "block_table"), block_table.shape[1], _ptr(free_pages, i32, "free_pages"),
+        free_pages.numel(), _ptr(free_start, i32, "free_start"), _stream()), "vsa_cache_release")
+
+
+def cache_append(k, v, slots, pages):
+    """Quantises k and v [T, Hkv, 128] bf16/fp16 (tokens may be strided) into the cache at their slots
+    (negative: not written)."""
+    n, Hkv, page_tokens = _pages_shape(pages)
+    code = _dtype_code(k, "k")
+    if v.dtype != k.dtype or v.shape != k.shape or k.dim() != 3 or k.shape[1] != Hkv:
+        raise ValueError(f"k and v must be [T, {Hkv}, 128] of one type, got {tuple(k.shape)} and {tuple(v.shape)}")
+    T, _, D = k.shape
+    if slots.shape != (T,):
+        raise ValueError(f"slots must be [{T}], got {tuple(slots.shape)}")
+    if T == 0:
+        return
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    _check(lib().vsa_cache_append_nvfp4(code, kp, vp, ks, vs, _ptr(slots, _torch().int32, "slots"), T, Hkv, D,
+                                        _ptr(pages, _torch().uint8, "pages"), n, page_tokens, _stream()),
+           "vsa_cache_append_nvfp4")
+
+
+def cache_read(slots, pages, dtype=None, k_out=None, v_out=None):
+    """The cached keys and values at the slots -> (k, v) [T, Hkv, 128]; rows of negative slots are left as they
+    were (zero in tensors made here)."""
+    torch = _torch()
+    n, Hkv, page_tokens = _pages_shape(pages)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T = slots.shape[0]
+    dtype = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
+    if k_out is None:
+        k_out = torch.zeros((T, Hkv, 128), dtype=dtype, device=pages.device)
+    if v_out is None:
+        v_out = torch.zeros((T, Hkv, 128), dtype=dtype, device=pages.device)
+    if k_out.shape != (T, Hkv, 128) or v_out.shape != (T, Hkv, 128):
+        raise ValueError(f"k_out and v_out must be [{T}, {Hkv}, 128]")
+    if T == 0:
+        return k_out, v_out
+    _check(lib().vsa_cache_read_nvfp4(_dtype_code(k_out, "k_out"), _ptr(slots, torch.int32, "slots"), T, Hkv, 128,
+                                      _ptr(pages, torch.uint8, "pages"), n, page_tokens, _ptr(k_out, dtype, "k_out"),
+                                      _ptr(v_out, dtype, "v_out"), _stream()), "vsa_cache_read_nvfp4")
+    return k_out, v_out
+
+
+def cache_workspace(max_q: int, Hq: int, Hkv: int, device="cuda"):
+    """The zeroed workspace of cache_attn calls with at most max_q new tokens a request."""
+    n = ctypes.c_size_t(0)
+    _check(lib().vsa_cache_attn_workspace(Hq, Hkv, max_q, ctypes.byref(n)), "vsa_cache_attn_workspace")
+    return _torch().zeros(n.value, dtype=_torch().uint8, device=device)
+
+
+def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal: bool = True, o_out=None,
+               lse_out=None):
+    """Attention of q [T, Hq, 128] (tokens may be strided) over each request's cached tokens -> (o [T, Hq, 128],
+    lse [T, Hq]).  Request r's queries are rows cu[r] .. cu[r+1]; causal: they are the cache's last tokens.
+    workspace: cache_workspace of at least this max_q and these heads; left ready for the next call."""
+    torch = _torch()
+    n, Hkv, page_tokens = _pages_shape(pages)
+    code = _dtype_code(q, "q")
+    qp, qs = _rows(q, "q")
+    T, Hq, D = q.shape
+    R = kv_len.shape[0]
+    if cu.shape != (R + 1,) or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("kv_len must be [R], cu [R + 1], block_table [R, max_pages]")
+    need = ctypes.c_size_t(0)
+    _check(lib().vsa_cache_attn_workspace(Hq, Hkv, max_q, ctypes.byref(need)), "vsa_cache_attn_workspace")
+    if workspace.numel() * workspace.element_size() < need.value:
+        raise ValueError(f"workspace needs {need.value} bytes (cache_workspace)")
+    if o_out is None:
+        o_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    if lse_out is None:
+        lse_out = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if o_out.shape != (T, Hq, D) or lse_out.shape != (T, Hq):
+        raise ValueError(f"o_out must be [{T}, {Hq}, {D}], lse_out [{T}, {Hq}]")
+    if T == 0:
+        return o_out, lse_out
+    i32 = torch.int32
+    _check(lib().vsa_cache_attn_nvfp4(
+        code, qp, qs, _ptr(cu, i32, "cu"), _ptr(kv_len, i32, "kv_len"), R, T, max_q, Hq, Hkv, D,
+        _ptr(pages, torch.uint8, "pages"), n, page_tokens, _ptr(block_table, i32, "block_table"),
+        block_table.shape[1], int(causal), _ptr(o_out, q.dtype, "o"), _ptr(lse_out, torch.float32, "lse"),
+        _ptr(workspace, workspace.dtype, "workspace"), _stream()), "vsa_cache_attn_nvfp4")
+    return o_out, lse_out
+
+
+def untile_merge(plan: Plan, ot, lse, o_past, lse_past, out=None, lse_out=None):
+    """o [B,S,H,D] and lse [B,S,H] of the union of two key sets: the fine stage's (ot [B,H,Sp,D], lse [B,H,Sp],
+    tiled) and another attention's (o_past [B,S,H,D], lse_past [B,S,H], untiled).  out and lse_out may be o_past
+    and lse_past."""
+    torch = _torch()
+    B, H, Sp, D = ot.shape
+    code = _dtype_code(ot, "o_tiled")
+    if Sp != plan.Sp:
+        raise ValueError(f"o_tiled has {Sp} rows, plan expects {plan.Sp}")
+    if o_past.shape != (B, plan.S, H, D) or lse_past.shape != (B, plan.S, H) or lse.shape != (B, H, Sp):
+        raise ValueError(f"o_past must be {(B, plan.S, H, D)}, lse_past {(B, plan.S, H)}, lse {(B, H, Sp)}")
+    if out is None:
+        out = torch.empty_like(o_past)
+    if lse_out is None:
+        lse_out = torch.empty_like(lse_past)
+    if out.shape != o_past.shape or lse_out.shape != lse_past.shape:
+        raise ValueError("out and lse_out must have the shapes of o_past and lse_past")
+    f32 = torch.float32
+    _check(lib().vsa_untile_merge(plan.handle, code, _ptr(ot, ot.dtype, "o_tiled"), _ptr(lse, f32, "lse"),
+                                  _ptr(o_past, ot.dtype, "o_past"), _ptr(lse_past, f32, "lse_past"), B, H, D,
+                                  _ptr(out, ot.dtype, "o"), _ptr(lse_out, f32, "lse_out"), _stream()),
+           "vsa_untile_merge")
+    return out, lse_out
+
+
 def get_status(stream=None) -> int:
     """Synchronise the stream, then read and clear the device status word."""
     torch = _torch()
@@ -499,6 +692,11 @@ class Forward:
     nvfp4=True runs the fine stage with NVFP4 q and k: the tiled q and k are
     quantised (two launches) and the FP4 attention kernel replaces the 16-bit
     one; v stays 16-bit.
+
+    past=(o_past [B,S,H,D], lse_past [B,S,H]) of a call joins an attention of
+    the same queries over other keys, such as KVCache.attend over the earlier
+    chunks of a video: untile_merge replaces untile, and the call returns o
+    and the lse [B,S,H] over both key sets.
     """
 
     def __init__(self, plan: Plan, B: int, H: int, topk: int | None, device="cuda", D: int = 128, dtype=None,
@@ -526,6 +724,7 @@ class Forward:
         if fused:
             self.ws = workspace(B, H, device)
         self.fws = torch.zeros(4, dtype=torch.int32, device=device)  # the fine stage's work queue
+        self.lse_all = None  # lse [B,S,H] of calls with a past
         if nvfp4:
             u8 = dict(dtype=torch.uint8, device=device)
             self.qc = torch.empty((B, H, plan.Sp, D // 2), **u8)
@@ -597,23 +796,29 @@ class Forward:
         self.quantize()
         self.attend()
 
-    def back(self, gate=None, out=None):
+    def back(self, gate=None, out=None, past=None):
         out = self.o if out is None else out
-        if self.gated:
+        if past is not None:
+            if self.gated:
+                raise ValueError("past applies to a Forward without the gate-compress branch")
+            _, self.lse_all = untile_merge(self.plan, self.ot, self.lse, past[0], past[1], out=out,
+                                           lse_out=self.lse_all)
+        elif self.gated:
             untile_gate(self.plan, self.ot, self.oc, gate, out=out)
         else:
             untile(self.plan, self.ot, out=out)
         return out
 
-    def __call__(self, q, k, v, block_map=None, gate=None, out=None, row_keep=None):
+    def __call__(self, q, k, v, block_map=None, gate=None, out=None, row_keep=None, past=None):
         """One forward step; o goes to `out` when given (else to self.o)."""
         if self.gated != (gate is not None):
             raise ValueError("a gate is required exactly when the Forward was built with gated=True")
         self.front(q, k, v, block_map, row_keep)
         self.fine()
-        return self.back(gate, out), self.lse
+        o = self.back(gate, out, past)
+        return o, (self.lse if past is None else self.lse_all)
 
-    def graph(self, q, k, v, block_map=None, gate=None, row_keep=None):
+    def graph(self, q, k, v, block_map=None, gate=None, row_keep=None, past=None):
         """Capture one forward step on these device tensors in a CUDA graph and
         return it (torch.cuda.CUDAGraph); replay() reruns the step's launches
         with the inputs read from the same buffers and o / lse written to
@@ -621,11 +826,11 @@ class Forward:
         set-up (device state, tensor-map encoder, kernel attributes) happens
         outside the capture."""
         torch = _torch()
-        self(q, k, v, block_map, gate, row_keep=row_keep)
+        self(q, k, v, block_map, gate, row_keep=row_keep, past=past)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            self(q, k, v, block_map, gate, row_keep=row_keep)
+            self(q, k, v, block_map, gate, row_keep=row_keep, past=past)
         return g
 
     def launches(self, block_map: bool = False) -> int:
@@ -634,6 +839,75 @@ class Forward:
         if self.fused:
             return 3 + quant + (1 if block_map else 0)  # front (+ map_to_index), attention, untile
         return 6 + quant + (1 if (self.gated and block_map) else 0)  # 3 tiles, index stage (+compress), attention, untile
+
+
+class KVCache:
+    """A 4-bit key/value cache of up to max_requests requests, its lengths and free pages kept on the device.
+
+    Each step: reserve(new_len, tokens) makes room for every request's new tokens, append(k, v) writes them (k, v
+    [tokens, Hkv, 128], request after request; rows past the last new token are padding), attend(q, max_q) attends
+    over the cache.  release(drop) ends requests.  Nothing synchronises with the host, and a step can be captured
+    in a CUDA graph; a request that does not fit is refused and sets VSA_ERR_CAPACITY (get_status).
+
+    A video made chunk by chunk: o_past = attend_chunk(q) over the earlier chunks, Forward(q, k, v, past=o_past) over
+    the current one, then reserve and append the chunk's k and v.
+    """
+
+    def __init__(self, num_pages: int, Hq: int, Hkv: int | None = None, max_requests: int = 1,
+                 max_len: int | None = None, page_tokens: int = 64, max_q: int = 1, device="cuda"):
+        torch = _torch()
+        self.Hq, self.Hkv, self.page_tokens, self.R = Hq, Hkv or Hq, page_tokens, max_requests
+        self.max_len = max_len or num_pages * page_tokens
+        self.pages = cache_pages(num_pages, self.Hkv, page_tokens, device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = torch.full((max_requests, -(-self.max_len // page_tokens)), -1, **i32)
+        self.free_pages = torch.arange(num_pages, **i32)
+        # [first free page, 3 unused, lengths]: one copy keeps a step's start while the step writes the next
+        self._state = torch.zeros(4 + max_requests, **i32)
+        self._start = torch.zeros_like(self._state)
+        self.kv_len, self.free_start = self._state[4:], self._state[:1]
+        self.cu = torch.zeros(max_requests + 1, **i32)
+        self.slots = None
+        self._slots = {}  # by row count: a captured step keeps its own
+        self.max_q = max_q
+        self.workspace = cache_workspace(max_q, Hq, self.Hkv, device)
+
+    def reserve(self, new_len, tokens: int):
+        """Room for new_len[r] (int32 [R] on the device) more tokens of each request, `tokens` rows in all with
+        padding; returns their slots."""
+        if tokens not in self._slots:
+            self._slots[tokens] = _torch().empty(tokens, dtype=_torch().int32, device=self.pages.device)
+        self.slots = self._slots[tokens]
+        self._start.copy_(self._state)
+        cache_tables(self._start[4:], new_len, self.page_tokens, self.free_pages, self._start[:1], self.table,
+                     self.slots, kv_len_out=self.kv_len, cu_out=self.cu, free_next_out=self.free_start)
+        return self.slots
+
+    def append(self, k, v):
+        """Writes k and v [tokens, Hkv, 128] at the slots of the last reserve."""
+        if self.slots is None:
+            raise ValueError("reserve comes before append")
+        cache_append(k, v, self.slots, self.pages)
+
+    def attend(self, q, causal: bool = True, cu=None, o_out=None, lse_out=None):
+        """q [tokens, Hq, 128], rows cu[r] .. cu[r+1] of request r (default: those of the last reserve), over the
+        cache -> (o, lse [tokens, Hq])."""
+        return cache_attn(q, self.cu if cu is None else cu, self.kv_len, self.table, self.pages, self.max_q,
+                          self.workspace, causal, o_out, lse_out)
+
+    def attend_chunk(self, q):
+        """q [R,S,Hq,128], the queries of each request's next chunk, over all its cached tokens -> (o [R,S,Hq,128],
+        lse [R,S,Hq])."""
+        R, S, H, D = q.shape
+        if R != self.R:
+            raise ValueError(f"q holds {R} requests, the cache {self.R}")
+        cu = _torch().arange(0, (R + 1) * S, S, dtype=_torch().int32, device=q.device) if S else self.cu * 0
+        o, lse = self.attend(q.view(R * S, H, D), causal=False, cu=cu)
+        return o.view(R, S, H, D), lse.view(R, S, H)
+
+    def release(self, drop):
+        """Ends the requests with drop[r] != 0 (bool or uint8 [R] on the device): their pages are free again."""
+        cache_release(drop, self.page_tokens, self.kv_len, self.table, self.free_pages, self.free_start)
 
 
 class HostPipeline:

@@ -1,0 +1,383 @@
+// cache.cu -- the 4-bit key/value cache outside its attention: block tables and
+// slot map of a growing batch, pages given back, tokens quantised into their
+// records, and read back.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cache.cuh"
+#include "cache_kernels.h"
+
+namespace vsa {
+
+namespace {
+
+using namespace cache;
+
+// ---------------------------------------------------------------------------
+// Block tables and slot map
+// ---------------------------------------------------------------------------
+//
+// Two prefix sums over the requests (their new tokens, their new pages) say
+// which request a token or a taken page belongs to.  Every CTA makes them for
+// itself in shared memory -- R <= 4096 lengths are 32 KB out of L2 -- and then
+// fills its share of the slots and of the new table entries, finding the
+// request by bisection; so the call is one launch with nothing to wait for.
+// The bound is latency: the largest call writes some MB.
+
+constexpr int kTabThreads = 512;
+constexpr int kTabSlots = kTabThreads * 4;  // slots of one pass of a CTA
+
+// Inclusive sum over the threads of a CTA of one value each.
+__device__ __forceinline__ long long block_scan(long long v, long long* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  __syncthreads();  // part may still be read from the scan before
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  long long before = 0;
+  for (int w = 0; w < warp; ++w) before += part[w];
+  return v + before;
+}
+
+// Largest i in [0, n) with a[i] <= x, given a[0] <= x.
+__device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_constant__ CacheTablesArgs a) {
+  extern __shared__ int tab_smem[];
+  __shared__ long long part[kTabThreads / 32];
+  __shared__ int s_pages;
+  int* tok = tab_smem;            // [R + 1] first new token
+  int* pag = tok + a.R + 1;       // [R + 1] first new page, from free_start
+  int* len = pag + a.R + 1;       // [R] cached tokens; -1: refused
+  const int per = (a.R + kTabThreads - 1) / kTabThreads;
+  const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
+  const int P = 1 << a.log_page;
+  const long long cap = static_cast<long long>(a.max_pages) << a.log_page;
+  const int start = __ldg(a.free_start);
+  const bool lead = blockIdx.x == 0;
+  if (threadIdx.x == 0) s_pages = 0;
+
+  // first new token of each request, cut at max_tokens
+  long long sum = 0;
+  for (int r = r0; r < r1; ++r) sum += max(__ldg(a.new_len + r), 0);
+  long long at = block_scan(sum, part) - sum;
+  for (int r = r0; r < r1; ++r) {
+    tok[r] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
+    at += max(__ldg(a.new_len + r), 0);
+    const int kv = __ldg(a.kv_len + r), nw = __ldg(a.new_len + r);
+    const bool fits = kv >= 0 && nw >= 0 && static_cast<long long>(kv) + nw <= cap && at <= a.max_tokens;
+    len[r] = fits ? kv : -1;
+  }
+  if (r0 < r1 && r1 == a.R) tok[a.R] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
+
+  // first new page of each request
+  auto pages_of = [&](int r) -> int {
+    const int kv = len[r];
+    if (kv < 0) return 0;
+    const long long end = static_cast<long long>(kv) + __ldg(a.new_len + r);
+    return static_cast<int>(((end + P - 1) >> a.log_page) - ((static_cast<long long>(kv) + P - 1) >> a.log_page));
+  };
+  sum = 0;
+  for (int r = r0; r < r1; ++r) sum += pages_of(r);
+  at = block_scan(sum, part) - sum;
+  // free pages; a free_start outside [0, n_free] leaves none
+  const long long have = start >= 0 && start <= a.n_free ? a.n_free - start : 0;
+  int taken = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int need = pages_of(r);
+    pag[r] = static_cast<int>(min(at, have));
+    at += need;
+    if (need > 0) {
+      if (at <= have) taken = static_cast<int>(at);
+      else len[r] = -1;
+    }
+    if (lead) {
+      const int kv = __ldg(a.kv_len + r);
+      const bool ok = len[r] >= 0;
+      a.kv_len_out[r] = ok ? kv + __ldg(a.new_len + r) : kv;
+      a.cu[r] = tok[r];
+      if (!ok) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_CAPACITY);
+    }
+  }
+  if (r0 < r1 && r1 == a.R) pag[a.R] = static_cast<int>(min(at, have));
+  if (taken > 0) atomicMax(&s_pages, taken);
+  __syncthreads();
+  const int pages = s_pages, tokens = tok[a.R];
+  if (lead && threadIdx.x == 0) {
+    a.cu[a.R] = tokens;
+    *a.free_next = start + pages;
+  }
+
+  // entries of the pages taken: page i of a request's new ones follows those it has
+  for (int e = blockIdx.x * kTabThreads + threadIdx.x; e < pages; e += gridDim.x * kTabThreads) {
+    const int r = last_at_most(pag, a.R, e);
+    const int had = (len[r] + P - 1) >> a.log_page;
+    a.table[static_cast<long long>(r) * a.max_pages + had + (e - pag[r])] = __ldg(a.free_pages + start + e);
+  }
+
+  // slots; a token of a page taken now reads its id from the stack, not from the entry above
+  const int page_limit = 0x7fffffff >> a.log_page;
+  for (long long i0 = static_cast<long long>(blockIdx.x) * kTabSlots + threadIdx.x * 4; i0 < a.max_tokens;
+       i0 += static_cast<long long>(gridDim.x) * kTabSlots) {
+    int4 out = make_int4(-1, -1, -1, -1);
+    int* ov = &out.x;
+    int r = i0 < tokens ? last_at_most(tok, a.R, static_cast<int>(i0)) : 0;
+    for (int j = 0; j < 4; ++j) {
+      const int i = static_cast<int>(i0) + j;
+      if (i >= tokens) break;
+      while (tok[r + 1] <= i) ++r;  // ends: tok[R] = tokens > i
+      if (len[r] < 0) continue;
+      const int pos = len[r] + (i - tok[r]);
+      const int pi = pos >> a.log_page, had = (len[r] + P - 1) >> a.log_page;
+      const int page = pi < had ? __ldg(a.table + static_cast<long long>(r) * a.max_pages + pi)
+                                : __ldg(a.free_pages + start + pag[r] + (pi - had));
+      if (page < 0 || page >= page_limit) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+      else ov[j] = (page << a.log_page) + (pos & (P - 1));
+    }
+    if (i0 + 4 <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slots + i0) = out;
+    } else {
+      for (int j = 0; i0 + j < a.max_tokens; ++j) a.slots[i0 + j] = ov[j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Pages given back
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kTabThreads) cache_release_kernel(const uint8_t* __restrict__ drop, int R,
+                                                                    int log_page, int32_t* kv_len,
+                                                                    const int32_t* __restrict__ table, int max_pages,
+                                                                    int32_t* free_pages, int n_free,
+                                                                    int32_t* free_start, unsigned int* status) {
+  extern __shared__ int tab_smem[];
+  __shared__ long long part[kTabThreads / 32];
+  __shared__ long long total;
+  int* pag = tab_smem;  // [R + 1] first page given back
+  const int per = (R + kTabThreads - 1) / kTabThreads;
+  const int r0 = min(static_cast<int>(threadIdx.x) * per, R), r1 = min(r0 + per, R);
+  const int P = 1 << log_page;
+  const long long cap = static_cast<long long>(max_pages) << log_page;
+  const int start = *free_start;
+  if (threadIdx.x == 0) total = 0;
+  auto pages_of = [&](int r) -> int {
+    if (!drop[r]) return 0;
+    const int kv = kv_len[r];
+    if (kv < 0 || kv > cap) {
+      atomicCAS(status, 0u, (unsigned)VSA_ERR_CAPACITY);
+      return 0;
+    }
+    return static_cast<int>((static_cast<long long>(kv) + P - 1) >> log_page);
+  };
+  long long sum = 0;
+  for (int r = r0; r < r1; ++r) sum += pages_of(r);
+  const long long incl = block_scan(sum, part);
+  if (threadIdx.x == kTabThreads - 1) total = incl;
+  __syncthreads();
+  const long long m = total;
+  if (start < 0 || start > n_free || m > start) {
+    if (threadIdx.x == 0) atomicCAS(status, 0u, (unsigned)VSA_ERR_CAPACITY);
+    return;  // the whole CTA
+  }
+  long long at = incl - sum;
+  for (int r = r0; r < r1; ++r) {
+    pag[r] = static_cast<int>(at);
+    at += pages_of(r);
+  }
+  if (threadIdx.x == 0) pag[R] = static_cast<int>(m);
+  __syncthreads();
+  const int base = start - static_cast<int>(m);
+  for (int e = threadIdx.x; e < static_cast<int>(m); e += kTabThreads) {
+    const int r = last_at_most(pag, R, e);
+    free_pages[base + e] = table[static_cast<long long>(r) * max_pages + (e - pag[r])];
+  }
+  for (int r = r0; r < r1; ++r)
+    if (drop[r]) kv_len[r] = 0;
+  if (threadIdx.x == 0) *free_start = base;
+}
+
+// ---------------------------------------------------------------------------
+// Append and read back
+// ---------------------------------------------------------------------------
+//
+// A CTA takes 16 tokens x 2 heads: a warp holds 4 tokens of a head, 8 threads a
+// token, a thread one 16-channel block of its K and of its V (64 bytes in, 16
+// bytes of codes and 2 scales out).  The scale of a block is the thread's own
+// maximum, so nothing is exchanged but the 8 K scales of a token, which become
+// one store.  Tokens are the warp's fast index because 16 tokens of a head
+// share a record: its lines are written from one CTA.
+// Bound: HBM (512 B in, 144 out a token and head).
+
+constexpr int kPutThreads = 256;
+constexpr int kPutTokens = 16, kPutHeads = 2;
+
+template <bool F16>
+__device__ __forceinline__ void unpack16(const uint4* src, float (&f)[16]) {
+  const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+  const uint32_t wd[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (F16) {
+      const float2 x = f16x2_to_f32(wd[i]);
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    } else {
+      f[2 * i] = bf16_lo(wd[i]);
+      f[2 * i + 1] = bf16_hi(wd[i]);
+    }
+  }
+}
+
+// Codes of 16 values and their scale byte: s = E4M3(fl32(amax / 6)), code =
+// E2M1(fl32(x * fl32(1 / s))), the rounding of vsa_quantize_nvfp4.
+__device__ __forceinline__ uint2 quantise16(const float (&f)[16], uint32_t& sb) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  sb = to_e4m3(__fdiv_rn(amax, 6.0f));
+  const float s = f16x2_to_f32(from_e4m3x2(sb)).x;
+  const float inv = s == 0.0f ? 0.0f : __frcp_rn(s);
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(f[i], inv);
+  return make_uint2(to_e2m1x8(y), to_e2m1x8(y + 8));
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kPutThreads) cache_append_kernel(
+    const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, long long k_stride, long long v_stride,
+    const int32_t* __restrict__ slots, int T, int Hkv, uint8_t* __restrict__ pages, int num_pages, int log_page,
+    unsigned int* status) {
+  const int g = threadIdx.x & 7;  // 16-channel block
+  const int t = blockIdx.x * kPutTokens + ((threadIdx.x >> 3) & 15);
+  const int h = blockIdx.y * kPutHeads + (threadIdx.x >> 7);
+  const bool in = t < T && h < Hkv;
+  const int slot = in ? __ldg(slots + t) : -1;
+  const bool bad = slot >= 0 && (slot >> log_page) >= num_pages;
+  if (bad && g == 0) atomicCAS(status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+  const bool put = slot >= 0 && !bad;
+  uint32_t ks = 0, vs = 0;
+  uint2 kc = make_uint2(0, 0), vc = make_uint2(0, 0);
+  if (put) {
+    float f[16];
+    unpack16<F16>(reinterpret_cast<const uint4*>(k + t * k_stride + h * 128 + g * 16), f);
+    kc = quantise16(f, ks);
+    unpack16<F16>(reinterpret_cast<const uint4*>(v + t * v_stride + h * 128 + g * 16), f);
+    vc = quantise16(f, vs);
+  }
+  // a token's eight K scales as two words
+  uint32_t word = ks;
+  word |= __shfl_down_sync(0xffffffffu, ks, 1) << 8;
+  word |= __shfl_down_sync(0xffffffffu, ks, 2) << 16;
+  word |= __shfl_down_sync(0xffffffffu, ks, 3) << 24;
+  if (!put) return;
+  const int p = slot & 15;
+  uint8_t* rec = pages + record_of(slot, h, Hkv, log_page);
+  reinterpret_cast<uint2*>(rec)[p * 8 + g] = kc;
+  reinterpret_cast<uint2*>(rec + kRecV)[p * 8 + g] = vc;
+  if ((g & 3) == 0) reinterpret_cast<uint32_t*>(rec + kRecKS)[p * 2 + (g >> 2)] = word;
+  rec[kRecVS + g * 16 + (p & 3) * 4 + (p >> 2)] = static_cast<uint8_t>(vs);
+}
+
+template <bool F16>
+__device__ __forceinline__ void store16(uint16_t* dst, uint2 codes, uint32_t sb) {
+  const uint32_t s = dup_lo(from_e4m3x2(sb));
+  uint32_t r[8];
+  from_e2m1x8(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&r[0]));
+  from_e2m1x8(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&r[4]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r[i] = mul_f16x2(r[i], s);
+    if (!F16) {
+      const float2 x = f16x2_to_f32(r[i]);
+      r[i] = pack_bf16x2(x.x, x.y);
+    }
+  }
+  reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kPutThreads) cache_read_kernel(const int32_t* __restrict__ slots, int T, int Hkv,
+                                                                 const uint8_t* __restrict__ pages, int num_pages,
+                                                                 int log_page, uint16_t* __restrict__ k,
+                                                                 uint16_t* __restrict__ v, unsigned int* status) {
+  const int g = threadIdx.x & 7;
+  const int t = blockIdx.x * kPutTokens + ((threadIdx.x >> 3) & 15);
+  const int h = blockIdx.y * kPutHeads + (threadIdx.x >> 7);
+  if (t >= T || h >= Hkv) return;
+  const int slot = __ldg(slots + t);
+  if (slot < 0) return;
+  if ((slot >> log_page) >= num_pages) {
+    if (g == 0) atomicCAS(status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+    return;
+  }
+  const int p = slot & 15;
+  const uint8_t* rec = pages + record_of(slot, h, Hkv, log_page);
+  const uint2 kc = __ldg(reinterpret_cast<const uint2*>(rec) + p * 8 + g);
+  const uint2 vc = __ldg(reinterpret_cast<const uint2*>(rec + kRecV) + p * 8 + g);
+  const uint32_t ks = __ldg(rec + kRecKS + p * 8 + g), vs = __ldg(rec + kRecVS + g * 16 + (p & 3) * 4 + (p >> 2));
+  const long long dst = (static_cast<long long>(t) * Hkv + h) * 128 + g * 16;
+  store16<F16>(k + dst, kc, ks);
+  store16<F16>(v + dst, vc, vs);
+}
+
+dim3 put_grid(int T, int Hkv) {
+  return dim3((T + kPutTokens - 1) / kPutTokens, (Hkv + kPutHeads - 1) / kPutHeads);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStream_t stream) {
+  const long long passes = (static_cast<long long>(a.max_tokens) + kTabSlots - 1) / kTabSlots;
+  const int grid = static_cast<int>(passes < 1 ? 1 : passes < num_sms ? passes : num_sms);
+  const int smem = (3 * a.R + 2) * 4;
+  if (smem > 40 * 1024) {  // more than the default limit only for R > 3400
+    cudaError_t e = cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (3 * kMaxRequests + 2) * 4);
+    if (e != cudaSuccess) return e;
+  }
+  cache_tables_kernel<<<grid, kTabThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_release(const uint8_t* drop, int R, int log_page, int32_t* kv_len, const int32_t* table,
+                                 int max_pages, int32_t* free_pages, int n_free, int32_t* free_start,
+                                 unsigned int* status, cudaStream_t stream) {
+  cache_release_kernel<<<1, kTabThreads, (R + 1) * 4, stream>>>(drop, R, log_page, kv_len, table, max_pages,
+                                                                free_pages, n_free, free_start, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(bool f16, const uint16_t* k, const uint16_t* v, long long k_stride,
+                                long long v_stride, const int32_t* slots, int T, int Hkv, uint8_t* pages,
+                                int num_pages, int log_page, unsigned int* status, cudaStream_t stream) {
+  if (T == 0) return cudaSuccess;
+  auto kern = f16 ? cache_append_kernel<true> : cache_append_kernel<false>;
+  kern<<<put_grid(T, Hkv), kPutThreads, 0, stream>>>(k, v, k_stride, v_stride, slots, T, Hkv, pages, num_pages,
+                                                     log_page, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(bool f16, const int32_t* slots, int T, int Hkv, const uint8_t* pages, int num_pages,
+                              int log_page, uint16_t* k, uint16_t* v, unsigned int* status, cudaStream_t stream) {
+  if (T == 0) return cudaSuccess;
+  auto kern = f16 ? cache_read_kernel<true> : cache_read_kernel<false>;
+  kern<<<put_grid(T, Hkv), kPutThreads, 0, stream>>>(slots, T, Hkv, pages, num_pages, log_page, k, v, status);
+  return cudaGetLastError();
+}
+
+}  // namespace vsa

@@ -1,0 +1,46 @@
+// cache_kernels.h -- internal launch entry points of the 4-bit key/value cache
+// and of the merge with the fine stage (not public ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "cache.cuh"
+#include "common.cuh"
+
+namespace vsa {
+
+// cache.cu
+struct CacheTablesArgs {
+  const int32_t *kv_len, *new_len;
+  int R, log_page;
+  const int32_t* free_pages;
+  int n_free;
+  const int32_t* free_start;
+  int32_t* table;
+  int max_pages;
+  int32_t *kv_len_out, *cu, *slots;
+  int max_tokens;
+  int32_t* free_next;
+  unsigned int* status;
+};
+cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_release(const uint8_t* drop, int R, int log_page, int32_t* kv_len, const int32_t* table,
+                                 int max_pages, int32_t* free_pages, int n_free, int32_t* free_start,
+                                 unsigned int* status, cudaStream_t stream);
+cudaError_t launch_cache_append(bool f16, const uint16_t* k, const uint16_t* v, long long k_stride,
+                                long long v_stride, const int32_t* slots, int T, int Hkv, uint8_t* pages,
+                                int num_pages, int log_page, unsigned int* status, cudaStream_t stream);
+cudaError_t launch_cache_read(bool f16, const int32_t* slots, int T, int Hkv, const uint8_t* pages, int num_pages,
+                              int log_page, uint16_t* k, uint16_t* v, unsigned int* status, cudaStream_t stream);
+
+// cache_attn.cu
+size_t cache_attn_workspace_bytes(int Hq, int Hkv, int max_q);
+cudaError_t launch_cache_attn(const cache::AttnArgs& a, bool f16, int max_q, int num_sms, cudaStream_t stream);
+
+// merge.cu
+cudaError_t launch_untile_merge(const Geo& g, int B, int H, const uint16_t* ot, const float* lse_t,
+                                const uint16_t* past, const float* lse_past, uint16_t* o, float* lse, bool f16,
+                                cudaStream_t stream);
+
+}  // namespace vsa

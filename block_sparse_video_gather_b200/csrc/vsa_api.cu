@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache_kernels.h"
 #include "kernels.h"
 #include "vsa.h"
 
@@ -578,6 +579,163 @@ int vsa_sparse_attn_bwd(vsa_plan_t plan, vsa_dtype_t dtype, const uint16_t* q, c
   return from_cuda(vsa::launch_attn_bwd(g, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// log2 of a page size the cache takes, or -1.
+int log_page_of(int page_tokens) {
+  return pow2(page_tokens) && page_tokens >= 16 && page_tokens <= 256 ? log2i(page_tokens) : -1;
+}
+
+// What every call on the cache's pages checks.
+int check_cache(int Hkv, int D, int num_pages, int page_tokens) {
+  if (Hkv < 1 || num_pages < 1) return VSA_ERR_INVALID_ARG;
+  if (D != 128 || Hkv > 65535 || log_page_of(page_tokens) < 0) return VSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * page_tokens > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
+  return VSA_OK;
+}
+}  // namespace
+
+int vsa_cache_page_bytes(int Hkv, int D, int page_tokens, size_t* bytes) {
+  if (!bytes) return VSA_ERR_INVALID_ARG;
+  if (int rc = check_cache(Hkv, D, 1, page_tokens)) return rc;
+  *bytes = static_cast<size_t>(Hkv) * (page_tokens / vsa::cache::kRecTokens) * vsa::cache::kRecBytes;
+  return VSA_OK;
+}
+
+int vsa_cache_tables(const int32_t* kv_len, const int32_t* new_len, int R, int page_tokens, const int32_t* free_pages,
+                     int n_free, const int32_t* free_start, int32_t* block_table, int max_pages, int32_t* kv_len_out,
+                     int32_t* cu, int32_t* slots, int max_tokens, int32_t* free_next, vsa_stream_t stream) {
+  if (!aligned16(kv_len) || !aligned16(new_len) || !aligned16(free_start) || !aligned16(block_table) ||
+      !aligned16(kv_len_out) || !aligned16(cu) || !aligned16(free_next))
+    return VSA_ERR_INVALID_ARG;
+  if ((n_free != 0 && !aligned16(free_pages)) || (max_tokens != 0 && !aligned16(slots))) return VSA_ERR_INVALID_ARG;
+  if (kv_len == kv_len_out || free_start == free_next) return VSA_ERR_INVALID_ARG;
+  if (R < 1 || n_free < 0 || max_pages < 1 || max_tokens < 0) return VSA_ERR_INVALID_ARG;
+  if (R > vsa::cache::kMaxRequests || log_page_of(page_tokens) < 0) return VSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_tokens > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  if (int rc = device_state(&ds)) return rc;
+  vsa::CacheTablesArgs a;
+  a.kv_len = kv_len;
+  a.new_len = new_len;
+  a.R = R;
+  a.log_page = log_page_of(page_tokens);
+  a.free_pages = free_pages;
+  a.n_free = n_free;
+  a.free_start = free_start;
+  a.table = block_table;
+  a.max_pages = max_pages;
+  a.kv_len_out = kv_len_out;
+  a.cu = cu;
+  a.slots = slots;
+  a.max_tokens = max_tokens;
+  a.free_next = free_next;
+  a.status = ds->status;
+  return from_cuda(vsa::launch_cache_tables(a, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int vsa_cache_release(const uint8_t* drop, int R, int page_tokens, int32_t* kv_len, const int32_t* block_table,
+                      int max_pages, int32_t* free_pages, int n_free, int32_t* free_start, vsa_stream_t stream) {
+  if (!aligned16(drop) || !aligned16(kv_len) || !aligned16(block_table) || !aligned16(free_pages) ||
+      !aligned16(free_start))
+    return VSA_ERR_INVALID_ARG;
+  if (R < 1 || n_free < 0 || max_pages < 1) return VSA_ERR_INVALID_ARG;
+  if (R > vsa::cache::kMaxRequests || log_page_of(page_tokens) < 0) return VSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_tokens > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  if (int rc = device_state(&ds)) return rc;
+  return from_cuda(vsa::launch_cache_release(drop, R, log_page_of(page_tokens), kv_len, block_table, max_pages,
+                                             free_pages, n_free, free_start, ds->status,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int vsa_cache_append_nvfp4(vsa_dtype_t dtype, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                           int64_t v_stride, const int32_t* slots, int T, int Hkv, int D, uint8_t* pages,
+                           int num_pages, int page_tokens, vsa_stream_t stream) {
+  if (dtype != VSA_BF16 && dtype != VSA_F16) return VSA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(pages) || T < 0) return VSA_ERR_INVALID_ARG;
+  if (int rc = check_cache(Hkv, D, num_pages, page_tokens)) return rc;
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  if (k_stride < row || v_stride < row || (k_stride & 7) || (v_stride & 7)) return VSA_ERR_INVALID_ARG;
+  DeviceState* ds = nullptr;
+  if (int rc = device_state(&ds)) return rc;
+  return from_cuda(vsa::launch_cache_append(dtype == VSA_F16, k, v, k_stride, v_stride, slots, T, Hkv, pages,
+                                            num_pages, log_page_of(page_tokens), ds->status,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int vsa_cache_read_nvfp4(vsa_dtype_t dtype, const int32_t* slots, int T, int Hkv, int D, const uint8_t* pages,
+                         int num_pages, int page_tokens, uint16_t* k, uint16_t* v, vsa_stream_t stream) {
+  if (dtype != VSA_BF16 && dtype != VSA_F16) return VSA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(pages) || T < 0) return VSA_ERR_INVALID_ARG;
+  if (int rc = check_cache(Hkv, D, num_pages, page_tokens)) return rc;
+  DeviceState* ds = nullptr;
+  if (int rc = device_state(&ds)) return rc;
+  return from_cuda(vsa::launch_cache_read(dtype == VSA_F16, slots, T, Hkv, pages, num_pages,
+                                          log_page_of(page_tokens), k, v, ds->status,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int vsa_cache_attn_workspace(int Hq, int Hkv, int max_q, size_t* bytes) {
+  if (!bytes || Hq < 1 || Hkv < 1 || max_q < 1 || Hq % Hkv != 0) return VSA_ERR_INVALID_ARG;
+  *bytes = vsa::cache_attn_workspace_bytes(Hq, Hkv, max_q);
+  return VSA_OK;
+}
+
+int vsa_cache_attn_nvfp4(vsa_dtype_t dtype, const uint16_t* q, int64_t q_stride, const int32_t* cu,
+                         const int32_t* kv_len, int R, int T, int max_q, int Hq, int Hkv, int D, const uint8_t* pages,
+                         int num_pages, int page_tokens, const int32_t* block_table, int max_pages, int causal,
+                         uint16_t* o, float* lse, void* workspace, vsa_stream_t stream) {
+  if (dtype != VSA_BF16 && dtype != VSA_F16) return VSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cu) || !aligned16(kv_len) || !aligned16(pages) || !aligned16(block_table) ||
+      !aligned16(o) || !aligned16(lse) || !aligned16(workspace))
+    return VSA_ERR_INVALID_ARG;
+  if (R < 1 || T < 0 || max_q < 1 || Hq < 1 || max_pages < 1) return VSA_ERR_INVALID_ARG;
+  if (int rc = check_cache(Hkv, D, num_pages, page_tokens)) return rc;
+  if (Hq % Hkv != 0 || q_stride < static_cast<int64_t>(Hq) * D || (q_stride & 7)) return VSA_ERR_INVALID_ARG;
+  if (R > vsa::cache::kMaxRequests) return VSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * Hq > 0x7fffffffLL || static_cast<long long>(max_pages) * page_tokens > 0x7fffffffLL)
+    return VSA_ERR_UNSUPPORTED;
+  DeviceState* ds = nullptr;
+  if (int rc = device_state(&ds)) return rc;
+  vsa::cache::AttnArgs a;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.cu = cu;
+  a.kv_len = kv_len;
+  a.R = R;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.pages = pages;
+  a.num_pages = num_pages;
+  a.log_page = log_page_of(page_tokens);
+  a.table = block_table;
+  a.max_pages = max_pages;
+  a.causal = causal != 0;
+  a.o = o;
+  a.lse = lse;
+  a.ws = workspace;
+  a.status = ds->status;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / 11.313708498984761);  // log2(e) / sqrt(128)
+  return from_cuda(vsa::launch_cache_attn(a, dtype == VSA_F16, max_q, ds->num_sms,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int vsa_untile_merge(vsa_plan_t plan, vsa_dtype_t dtype, const uint16_t* o_tiled, const float* lse_tiled,
+                     const uint16_t* o_past, const float* lse_past, int B, int H, int D, uint16_t* o, float* lse,
+                     vsa_stream_t stream) {
+  if (dtype != VSA_BF16 && dtype != VSA_F16) return VSA_ERR_INVALID_ARG;
+  if (!plan || !aligned16(o_tiled) || !aligned16(lse_tiled) || !aligned16(o_past) || !aligned16(lse_past) ||
+      !aligned16(o) || (lse && !aligned16(lse)))
+    return VSA_ERR_INVALID_ARG;
+  if (int rc = check_dims(B, H, D)) return rc;
+  DeviceState* ds = nullptr;
+  if (int rc = device_state(&ds)) return rc;
+  return from_cuda(vsa::launch_untile_merge(plan->g, B, H, o_tiled, lse_tiled, o_past, lse_past, o, lse,
+                                            dtype == VSA_F16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int vsa_get_status(vsa_stream_t stream, int* device_status) {
   if (!device_status) return VSA_ERR_INVALID_ARG;
   DeviceState* ds = nullptr;
@@ -602,6 +760,7 @@ const char* vsa_strerror(int status) {
     case VSA_ERR_BAD_INDEX: return "device: block id outside [0, num_blocks) or count outside [0, max_k]";
     case VSA_ERR_TIMEOUT: return "device: a pipeline wait ran out and the kernel stopped early";
     case VSA_ERR_NO_DEVICE: return "no usable CUDA device";
+    case VSA_ERR_CAPACITY: return "device: a cache request did not fit (lengths, block table, free pages, token batch)";
     default: return "unknown status";
   }
 }

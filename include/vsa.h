@@ -44,7 +44,8 @@
  *    by the caller; the library allocates no device memory in any call.
  *  - Every call is asynchronous on `stream` and returns an int status.  A
  *    rejected argument returns before any device work is queued.  Errors found on the device
- *    (bad block ids, counts above max_k, a pipeline wait that ran out) are
+ *    (bad block ids, counts above max_k, cache requests that do not fit, a
+ *    pipeline wait that ran out) are
  *    recorded in a per-device status word read by vsa_get_status().
  *  - Nothing falls back: unsupported input is an error, never rerouted.
  */
@@ -83,7 +84,8 @@ enum vsa_status {
     VSA_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
     VSA_ERR_BAD_INDEX = 5,     /* device: a block id outside [0, NB) or a count outside [0, max_k] */
     VSA_ERR_TIMEOUT = 6,       /* device: a pipeline wait ran out; the kernel stopped early */
-    VSA_ERR_NO_DEVICE = 7      /* no usable CUDA device */
+    VSA_ERR_NO_DEVICE = 7,     /* no usable CUDA device */
+    VSA_ERR_CAPACITY = 8       /* device: a request did not fit the cache's tables, pages or token batch */
 };
 
 /*
@@ -416,10 +418,159 @@ VSA_API int vsa_sparse_attn_bwd(vsa_plan_t plan, vsa_dtype_t dtype, const uint16
                                 const int32_t *q2k_idx, const int32_t *q2k_num, int max_k, int B, int H, int D,
                                 uint16_t *dq, uint16_t *dk, uint16_t *dv, void *workspace, vsa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The 4-bit key/value cache.  The pages have no counterpart: a causal or
+ * chunk-by-chunk video model caches keys and values, and this library keeps
+ * them in the NVFP4 format of vsa_quantize_nvfp4 (E2M1 codes, one E4M3 scale
+ * per 16 channels, the same rounding), K and V alike: 144 bytes a token and
+ * head in place of 512.
+ *
+ *   pages  [num_pages, Hkv, page_tokens / 16, 2304] bytes, caller-owned,
+ *          16-byte aligned; page_tokens is 16, 32, 64, 128 or 256, num_pages *
+ *          page_tokens < 2^31.  Their contents need not be initialised.
+ *   record 2304 bytes, the 16 tokens t = 0 .. 15 of a page and head:
+ *            [   0,1024)  K codes, 64 bytes a token, channel 2j in the low
+ *                         nibble of byte j, 2j+1 in the high nibble
+ *            [1024,2048)  V codes, the same
+ *            [2048,2176)  K scales, byte 8 t + g for channels 16g .. 16g+15
+ *            [2176,2304)  V scales, byte 16 g + 4 (t % 4) + t / 4
+ *   slot   a token's place: page * page_tokens + its place in the page
+ *   request r (0 <= r < R) holds kv_len[r] tokens: position i is in page
+ *          block_table[r][i / page_tokens].  block_table [R, max_pages] int32;
+ *          entries past a request's last page are not read.
+ *   cu     [R + 1] int32, the first of each request's new tokens in the batch
+ *          of new tokens (request after request), cu[R] their number
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one page: Hkv * page_tokens * 144. */
+VSA_API int vsa_cache_page_bytes(int Hkv, int D, int page_tokens, size_t *bytes);
+
+/*
+ * Block tables and slot map of a batch of requests that grow by new_len[r]
+ * tokens each.  With P = page_tokens, request r gets
+ *   n_r = ceil((kv_len[r] + new_len[r]) / P) - ceil(kv_len[r] / P)
+ * pages, taken in request order from free_pages[*free_start ..], and its new
+ * token i the slot of position kv_len[r] + i.
+ *   kv_len, new_len : [R] int32, 1 <= R <= 4096
+ *   free_pages      : [n_free] int32 page ids, a stack: those below
+ *                     *free_start are in use (NULL where n_free = 0)
+ *   free_start      : 1 int32 on the device
+ *   block_table     : [R, max_pages] int32, in and out: the new pages'
+ *                     entries are written, no other
+ *   kv_len_out      : [R] int32, kv_len[r] + new_len[r]
+ *   cu              : [R + 1] int32, prefix sums of new_len
+ *   slots           : [max_tokens] int32 (NULL where max_tokens = 0); -1 past
+ *                     the last new token
+ *   free_next       : 1 int32, *free_start plus the pages taken
+ * A request that cannot be served -- a negative length, more than max_pages
+ * pages, no free pages left for it, or tokens past max_tokens -- is refused as
+ * a whole: it takes no page, its slots are -1, kv_len_out[r] = kv_len[r], and
+ * the status word gets VSA_ERR_CAPACITY.  Pages run out in request order: once
+ * one request is refused for want of pages, so is every later one that needs any.
+ * cu holds the sums of max(new_len, 0) whether or not a request was refused,
+ * cut at max_tokens.
+ * kv_len_out and free_next must not be the arrays kv_len and free_start (other
+ * thread blocks still read those): VSA_ERR_INVALID_ARG.
+ */
+VSA_API int vsa_cache_tables(const int32_t *kv_len, const int32_t *new_len, int R, int page_tokens,
+                             const int32_t *free_pages, int n_free, const int32_t *free_start, int32_t *block_table,
+                             int max_pages, int32_t *kv_len_out, int32_t *cu, int32_t *slots, int max_tokens,
+                             int32_t *free_next, vsa_stream_t stream);
+
+/*
+ * The way back: every request r with drop[r] != 0 gives its ceil(kv_len[r] /
+ * P) pages back and gets kv_len[r] = 0.  The pages are written, request after
+ * request, to free_pages[*free_start - m .. *free_start) (m of them in all),
+ * and *free_start becomes *free_start - m.  In place; one thread block.
+ * A kv_len outside [0, max_pages * P] counts as 0 pages, and when m exceeds
+ * *free_start nothing is released; both set VSA_ERR_CAPACITY.
+ *   drop : [R] bytes, 1 <= R <= 4096;  kv_len, free_pages, free_start as above
+ */
+VSA_API int vsa_cache_release(const uint8_t *drop, int R, int page_tokens, int32_t *kv_len,
+                              const int32_t *block_table, int max_pages, int32_t *free_pages, int n_free,
+                              int32_t *free_start, vsa_stream_t stream);
+
+/*
+ * Append: k, v [T, Hkv, D] dtype are quantised and written at their slots.
+ *   k_stride, v_stride : elements from one token to the next, at least Hkv *
+ *                        D and a multiple of 8 (a slice of a fused projection
+ *                        needs no copy); heads and channels are contiguous
+ *   slots : [T] int32 (vsa_cache_tables); a negative slot's token is not
+ *           written.  Slots of one call must differ: where two tokens share
+ *           one, which bytes of each remain is unspecified.
+ * Values beyond 2688 = 448 * 6 in magnitude saturate, infinities too; a NaN is
+ * stored as some finite value.  T = 0 does nothing.
+ * A slot >= num_pages * page_tokens is not written and sets VSA_ERR_BAD_INDEX.
+ */
+VSA_API int vsa_cache_append_nvfp4(vsa_dtype_t dtype, const uint16_t *k, const uint16_t *v, int64_t k_stride,
+                                   int64_t v_stride, const int32_t *slots, int T, int Hkv, int D, uint8_t *pages,
+                                   int num_pages, int page_tokens, vsa_stream_t stream);
+
+/*
+ * Read back: k, v [T, Hkv, D] dtype receive the values that the codes at the
+ * slots stand for (every one is exact in bf16 and in fp16).  Rows of negative
+ * slots are left as they were; a slot >= num_pages * page_tokens too, and it
+ * sets VSA_ERR_BAD_INDEX.
+ */
+VSA_API int vsa_cache_read_nvfp4(vsa_dtype_t dtype, const int32_t *slots, int T, int Hkv, int D,
+                                 const uint8_t *pages, int num_pages, int page_tokens, uint16_t *k, uint16_t *v,
+                                 vsa_stream_t stream);
+
+/*
+ * Attention over the cache.  Query token i (0 <= i < n_r = cu[r+1] - cu[r]) of
+ * request r, query head h, over the cached positions j of key head h / (Hq / Hkv):
+ *   o = sum_j softmax_j(D^-1/2 q . k_j) v_j,   lse = log sum_j exp(D^-1/2 q . k_j)
+ * with j < kv_len[r], and with causal != 0 also j <= kv_len[r] - n_r + i (the
+ * new tokens are the cache's last n_r).  A row that sees no position gives
+ * o = 0 and lse = -inf.
+ *   q        : [T, Hq, D] dtype, q_stride elements from token to token (at
+ *              least Hq * D, a multiple of 8)
+ *   cu       : [R + 1] int32, ascending within [0, T];  kv_len: [R] int32
+ *   R        : 1 .. 4096;  Hq a multiple of Hkv;  T * Hq < 2^31
+ *   max_q    : the largest n_r, or an upper bound: it selects the kernel, and
+ *              a bound that does not hold costs speed, not results
+ *   o        : [T, Hq, D] dtype, lse: [T, Hq] fp32; rows outside every
+ *              request are left as they were
+ *   workspace: vsa_cache_attn_workspace bytes, zero before the first call;
+ *              each call leaves its counters zero unless it reports
+ *              VSA_ERR_TIMEOUT, after which the caller zeroes it again.  Calls
+ *              that share a workspace must not run concurrently (two captured
+ *              graphs that do not overlap may share one).
+ * The codes' values, q (bf16: times a power of two per row) and the softmax
+ * numerators enter the products as fp16, which holds all but the numerators
+ * exactly; sums are fp32.
+ * Device-side checks, each setting VSA_ERR_BAD_INDEX: positions in pages
+ * outside [0, num_pages) are left out; kv_len is cut to [0, max_pages *
+ * page_tokens], cu to ascending values within [0, T].
+ */
+VSA_API int vsa_cache_attn_workspace(int Hq, int Hkv, int max_q, size_t *bytes);
+VSA_API int vsa_cache_attn_nvfp4(vsa_dtype_t dtype, const uint16_t *q, int64_t q_stride, const int32_t *cu,
+                                 const int32_t *kv_len, int R, int T, int max_q, int Hq, int Hkv, int D,
+                                 const uint8_t *pages, int num_pages, int page_tokens, const int32_t *block_table,
+                                 int max_pages, int causal, uint16_t *o, float *lse, void *workspace,
+                                 vsa_stream_t stream);
+
+/*
+ * Untile fused with the merge of the fine stage and an attention over other
+ * keys (vsa_cache_attn_nvfp4 over the past): for every real token s,
+ *   lse = log(exp(l1) + exp(l2)),
+ *   o[b,s,h,:] = exp(l1 - lse) o_tiled[b,h,slot(s),:] + exp(l2 - lse) o_past[b,s,h,:]
+ * with l1 = lse_tiled[b,h,slot(s)] and l2 = lse_past[b,s,h], the attention over
+ * the union of the two key sets; fp32, o rounded once.
+ *   o_tiled, lse_tiled : [B,H,Sp,D] dtype and [B,H,Sp] fp32 (the fine stage's)
+ *   o_past, lse_past   : [B,S,H,D] dtype and [B,S,H] fp32
+ *   o, lse             : [B,S,H,D] dtype and [B,S,H] fp32 (lse may be NULL);
+ *                        they may be o_past and lse_past themselves
+ * lse of -inf: that side has no key and its o is not used; both: o = 0, lse = -inf.
+ */
+VSA_API int vsa_untile_merge(vsa_plan_t plan, vsa_dtype_t dtype, const uint16_t *o_tiled, const float *lse_tiled,
+                             const uint16_t *o_past, const float *lse_past, int B, int H, int D, uint16_t *o,
+                             float *lse, vsa_stream_t stream);
+
 /*
  * Synchronise `stream`, then read and clear the status word of the current
  * device: *device_status receives VSA_OK or the first device-detected error
- * (VSA_ERR_BAD_INDEX, VSA_ERR_TIMEOUT) since the last read.
+ * (VSA_ERR_BAD_INDEX, VSA_ERR_TIMEOUT, VSA_ERR_CAPACITY) since the last read.
  */
 VSA_API int vsa_get_status(vsa_stream_t stream, int *device_status);
 
