@@ -38,6 +38,12 @@ cudaError_t launch_cache_read(bool f16, const int32_t* slots, int T, int Hkv, co
 size_t cache_attn_workspace_bytes(int Hq, int Hkv, int max_q);
 cudaError_t launch_cache_attn(const cache::AttnArgs& a, bool f16, int max_q, int num_sms, cudaStream_t stream);
 
+// cache_attn_small.cu: requests of more than `over` and at most `upto` rows (new tokens x query heads of a key
+// head); `rows`: the largest number expected, which selects the row tile.
+size_t cache_attn_small_workspace(int num_workers);
+cudaError_t launch_cache_attn_small(const cache::AttnArgs& a, int over, int upto, bool f16, int rows, int num_sms,
+                                    cudaStream_t stream);
+
 // merge.cu
 cudaError_t launch_untile_merge(const Geo& g, int B, int H, const uint16_t* ot, const float* lse_t,
                                 const uint16_t* past, const float* lse_past, uint16_t* o, float* lse, bool f16,

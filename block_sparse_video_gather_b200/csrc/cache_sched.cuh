@@ -1,0 +1,175 @@
+// cache_sched.cuh -- how the attention kernels of the 4-bit cache divide a batch.
+//
+// The rows of a request and key head are its new tokens times the query heads
+// that share the key head, row = token * G + head in the group, cut into tiles
+// of RT rows; an item is one (request, key head, tile).  Its cached tokens, as
+// far as the tile's last row sees them, are cut into units of KT keys (an item
+// that sees nothing has one unit, which writes its rows).  All units of the
+// batch in item order form one line, and worker i of N takes [U i / N, U (i + 1)
+// / N): lengths as uneven as they may be, each worker reads the same amount to
+// within a unit.  Items that end up in several workers are joined by their
+// running maxima and sums.  Every worker finds its place by itself from cu and
+// kv_len, so lengths stay on the device and a captured call takes new ones.
+#pragma once
+
+#include "cache.cuh"
+
+namespace vsa {
+namespace cache {
+
+// sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m > 0: the Euclid-like
+// recursion on (m, a) for counting lattice points under a line.
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+template <int RT, int KT>
+struct Sched {
+  static __device__ __forceinline__ int tiles(const AttnArgs& a, const Request& q) { return (q.n * a.G + RT - 1) / RT; }
+  // Cached tokens that tile j's last row sees.
+  static __device__ __forceinline__ int keys(const AttnArgs& a, const Request& q, int j) {
+    const int last = min((j + 1) * RT, q.n * a.G) - 1;
+    return visible(a, q, last / a.G);
+  }
+  static __device__ __forceinline__ int units(const AttnArgs& a, const Request& q, int j) {
+    return max(1, (keys(a, q, j) + KT - 1) / KT);
+  }
+  // Units of tiles 0 .. j-1.
+  static __device__ __forceinline__ long long units_before(const AttnArgs& a, const Request& q, int j) {
+    if (!a.causal) return static_cast<long long>(max(1, (q.kv + KT - 1) / KT)) * j;
+    if (j <= 1) return j == 0 ? 0 : units(a, q, 0);
+    // whole tiles i: the last row's token is floor((RT (i + 1) - 1) / G), it sees kv - n + 1 more than that many
+    // tokens, which is floor((RT (i + 1) - 1 + G (kv - n + KT)) / (G KT)) units, or 1 where that is less
+    const int whole = (q.n * a.G) / RT, n = min(j, whole);
+    const long long G = a.G, c = q.kv - q.n;
+    const long long short_of = 1 - G * c;  // RT (i + 1) must reach this for the first whole unit
+    const long long i0 = min(static_cast<long long>(n), short_of <= RT ? 0 : (short_of + RT - 1) / RT - 1);
+    long long s = i0 + floor_sum(n - i0, G * KT, RT, RT * (i0 + 1) - 1 + G * (c + KT));
+    if (j > whole) s += units(a, q, whole);
+    return s;
+  }
+};
+
+// Which requests a kernel takes: those of more than `over` and at most `upto` rows a key head.
+struct Share {
+  int over, upto;
+};
+__device__ __forceinline__ bool takes(const Share& s, const AttnArgs& a, const Request& q) {
+  const int rows = q.n * a.G;
+  return rows > s.over && rows <= s.upto;
+}
+
+// Units of each request, summed: pre[r] = units of requests 0 .. r-1, pre[R] = U.
+// All threads of the CTA; ends with a barrier.
+template <class S, int THREADS>
+__device__ __forceinline__ void scan_units(const AttnArgs& a, const Share& share, long long* pre, long long* part) {
+  const int per = (a.R + THREADS - 1) / THREADS;
+  const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
+  const bool report = blockIdx.x == 0;
+  long long sum = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Request q = load_request(a, r, report);
+    pre[r] = sum;
+    if (takes(share, a, q)) sum += S::units_before(a, q, S::tiles(a, q)) * a.Hkv;
+  }
+  long long v = sum;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  long long before = v - sum;
+  for (int w = 0; w < warp; ++w) before += part[w];
+  for (int r = r0; r < r1; ++r) pre[r] += before;
+  if (threadIdx.x == THREADS - 1) pre[a.R] = before + sum;
+  __syncthreads();
+}
+
+// A place in the line of units.
+template <class S>
+struct Cursor {
+  int r, h, j;         // item
+  int k, nu;           // unit in it, and its units
+  int nt;              // tiles of the request
+  Request req;
+  long long item0;     // the item's first unit in the line
+
+  // Unit u of the line; pre from scan_units.
+  __device__ __forceinline__ void seek(const AttnArgs& a, const long long* pre, long long u) {
+    int lo = 0, hi = a.R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    r = lo;
+    req = load_request(a, r, false);
+    nt = S::tiles(a, req);
+    const long long head = S::units_before(a, req, nt);
+    long long rem = u - pre[r];
+    h = static_cast<int>(rem / head);
+    rem -= h * head;
+    int tl = 0, th = nt;
+    while (th - tl > 1) {
+      const int mid = (tl + th) >> 1;
+      if (S::units_before(a, req, mid) <= rem) tl = mid;
+      else th = mid;
+    }
+    j = tl;
+    k = static_cast<int>(rem - S::units_before(a, req, j));
+    nu = S::units(a, req, j);
+    item0 = u - k;
+  }
+  // The next item; the caller knows that there is one.
+  __device__ __forceinline__ void next_item(const AttnArgs& a, const Share& share) {
+    item0 += nu;
+    k = 0;
+    if (++j == nt) {
+      j = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        do {
+          ++r;
+          req = load_request(a, r, false);
+        } while (r + 1 < a.R && !takes(share, a, req));
+        nt = S::tiles(a, req);
+      }
+    }
+    nu = S::units(a, req, j);
+  }
+};
+
+// Worker i of n over U units; and the worker that holds unit u.
+__device__ __forceinline__ long long range_start(long long U, int i, int n) { return U * i / n; }
+__device__ __forceinline__ int worker_of(long long U, long long u, int n) {
+  return static_cast<int>(((u + 1) * n - 1) / U);
+}
+
+// Workspace: counters of joined items, then the workers' parts.  A worker's
+// range cuts at most two items, its first (slot 0) and the one that starts in
+// it and goes on (slot 1); a part holds RT rows of 128 sums, then RT maxima and
+// RT denominators.
+constexpr int kMaxWorkers = 1024;
+template <int RT>
+__host__ __device__ constexpr size_t part_floats() {
+  return static_cast<size_t>(RT) * 130;
+}
+
+}  // namespace cache
+}  // namespace vsa
