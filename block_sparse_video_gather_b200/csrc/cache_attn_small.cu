@@ -4,10 +4,10 @@
 // Bound: HBM.  A cached token and head are 144 bytes, 0.022 ns at 6561 GB/s;
 // the work beside the loads is to make 256 fp16 values of them.  What the
 // design does about both:
-//  - The line of 16-token units (cache_sched.cuh) is cut evenly over the CTAs,
+//  - The line of 32-token units (cache_sched.cuh) is cut evenly over the CTAs,
 //    one per SM, and a CTA's share evenly over its warps.  A warp works alone:
-//    its own ring of records (one bulk copy of 2304 bytes each, four in
-//    flight, 36 KB or more per SM), its own softmax state.
+//    its own ring of two units (a bulk copy of 4608 bytes each, or two where a
+//    page ends between), its own softmax state.
 //  - Rows are the narrow side of the products: S^T = K Q^T and O^T = V^T P^T
 //    with m16n8k16, 16 keys or channels by 8 rows.  At one row to a key head
 //    that leaves 7/8 of a product unused, and the tensor pipe still idles; the
@@ -39,9 +39,10 @@ namespace {
 
 using namespace cache;
 
-constexpr int kStages = 4;                       // records in flight per warp
+constexpr int kUnit = 32;                        // keys of a unit: two records
+constexpr int kUnitBytes = 2 * kRecBytes;
 constexpr uint64_t kTimeoutNs = 2000000000ull;   // 2 s per wait
-constexpr int kMinUnits = 4;                     // units a warp gets at least
+constexpr int kMinUnits = 2;                     // units a warp gets at least
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -64,45 +65,59 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // Part of an item that a warp or CTA holds; item0 < 0: none.
 struct PieceMeta {
   long long item0;
-  int nu, r, h, j;
+  int nu, h, j;
+  int q0, rows;  // the request's first new token, the item's rows
 };
 
-template <int NT, int W>
+template <int NT, int W, int STAGES>
 struct Smem {
   static constexpr int kRows = 8 * NT;
   static constexpr size_t kPieceBytes = part_floats<kRows>() * 4;
-  alignas(16) uint8_t ring[W][kStages][kRecBytes];
+  alignas(16) uint8_t ring[W][STAGES][kUnitBytes];
   alignas(16) uint8_t piece[W][kPieceBytes];  // a warp's first item, begun before its range
   PieceMeta meta[2 * W];                      // [2 w]: that item, [2 w + 1]: one that goes on after its range
   long long part[W];
-  uint64_t full[W][kStages];
-  int have[W][kStages];  // 1: the record was loaded
+  uint64_t full[W][STAGES];
   int abort;
-  int join[2];
+  int join[2][2];  // items this CTA joins: first and last CTA, or -1
 };
 
-// One row of a part: 128 sums (4 to a lane), maximum and denominator.
+// One row of a part: 128 sums (4 to a lane), maximum and denominator; w: the
+// weight of the part that this lane looks after.
 struct RowPart {
   float4 o;
-  float m, l;
+  float m, l, w;
 };
-__device__ __forceinline__ void add_part(RowPart& t, float4 o, float w, float l) {
+// Weight of a part with maximum m under the joint maximum.  Without a maximum a
+// part has nothing but zeros, or the NaN of its scores.
+__device__ __forceinline__ float part_weight(float m, float joint) {
+  return m == -INFINITY ? 1.0f : ex2_approx(m - joint);
+}
+// Joint maximum and denominator of up to 32 parts, one a lane (absent: -inf, 0).
+__device__ __forceinline__ RowPart join_weights(float m, float l) {
+  RowPart t;
+  t.m = m;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) t.m = fmaxf(t.m, __shfl_xor_sync(0xffffffffu, t.m, d));
+  t.w = part_weight(m, t.m);
+  t.l = t.w * l;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) t.l += __shfl_xor_sync(0xffffffffu, t.l, d);
+  t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  return t;
+}
+__device__ __forceinline__ void add_part(RowPart& t, float4 o, float w) {
   t.o.x += w * o.x;
   t.o.y += w * o.y;
   t.o.z += w * o.z;
   t.o.w += w * o.w;
-  t.l += w * l;
-}
-// Weight of a part with maximum m under the joint maximum.
-__device__ __forceinline__ float part_weight(float m, float joint) {
-  return m == -INFINITY ? 0.0f : ex2_approx(m - joint);
 }
 
 template <bool F16>
-__device__ __forceinline__ void write_row(const AttnArgs& a, const Request& req, int h, int row, const RowPart& t) {
+__device__ __forceinline__ void write_row(const AttnArgs& a, const PieceMeta& mt, int row, const RowPart& t) {
   const int lane = threadIdx.x & 31;
   const int token = row / a.G;
-  const long long dst = (static_cast<long long>(req.q0) + token) * a.Hq + h * a.G + (row - token * a.G);
+  const long long dst = (static_cast<long long>(mt.q0) + token) * a.Hq + mt.h * a.G + (row - token * a.G);
   const float inv = t.l != 0.0f ? 1.0f / t.l : 0.0f;
   uint2 w;
   w.x = pack_half2<F16>(t.o.x * inv, t.o.y * inv);
@@ -111,96 +126,127 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, const Request& req,
   if (lane == 0) a.lse[dst] = t.l != 0.0f ? (t.m + __log2f(t.l)) * 0.69314718055994531f : -INFINITY;
 }
 
-template <int NT, bool F16, int W>
+template <int NT, bool F16, int W, int STAGES>
 __global__ void __launch_bounds__(W * 32, 1)
     cache_attn_small_kernel(const __grid_constant__ AttnArgs a, const Share share) {
   constexpr int RT = 8 * NT;
-  using S = Sched<RT, kRecTokens>;
-  using Sm = Smem<NT, W>;
+  using S = Sched<RT, kUnit>;
+  using Sm = Smem<NT, W, STAGES>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
 
   if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[warp][s], 1);
+    for (int s = 0; s < STAGES; ++s) mbar_init(&sm.full[warp][s], 1);
     sm.meta[2 * warp].item0 = sm.meta[2 * warp + 1].item0 = -1;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
   if (threadIdx.x == 0) {
     sm.abort = 0;
-    sm.join[0] = sm.join[1] = 0;
+    sm.join[0][0] = sm.join[1][0] = -1;
   }
-  // the sums over requests take the place of the warps' pieces until every warp has found its own
+  // the sums over many requests take the place of the warps' pieces until every warp has found its own
   long long* pre = reinterpret_cast<long long*>(&sm.piece[0][0]);
   static_assert(sizeof(sm.piece) >= (kMaxRequests + 1) * 8, "the requests' sums must fit");
-  scan_units<S, W * 32>(a, share, pre, sm.part);
-  const long long U = pre[a.R];
+  const Line line = make_line<S, W * 32>(a, share, pre, sm.part);
+  const long long U = line.total;
   if (U == 0) return;
   const long long wanted = (U + W * kMinUnits - 1) / (W * kMinUnits);
   const int N = wanted < gridDim.x ? static_cast<int>(wanted) : static_cast<int>(gridDim.x);
   const int cta = blockIdx.x;
   if (cta >= N) return;
-  const long long cs = range_start(U, cta, N), ce = range_start(U, cta + 1, N);
-  const long long ws = cs + (ce - cs) * warp / W, we = cs + (ce - cs) * (warp + 1) / W;
-  const int total = static_cast<int>(we - ws);
+  const Cut cut(U, N);
+  const long long cs = cut.start(cta), ce = cut.start(cta + 1);
+  const int mine = static_cast<int>(ce - cs);
+  const int ws = static_cast<long long>(mine) * warp / W, we = static_cast<long long>(mine) * (warp + 1) / W;
+  const int total = we - ws;
 
   Cursor<S> cc;
-  if (total > 0) cc.seek(a, pre, ws);
-  __syncthreads();
+  if (total > 0) cc.seek(a, line, cs + ws);
+  __syncthreads();  // the sums over requests are no longer needed; the flags above are set
 
   bool ok = true;
   int issued = 0;
   if (total > 0) {
-    // ---- loads: a cursor of their own, kStages units ahead
+    // ---- loads: a cursor of their own, STAGES units ahead
     Cursor<S> lc = cc;
     int lkeys = S::keys(a, lc.req, lc.j);
     int cache_r = -1, cache_p = 0, my_page = -1;  // 32 entries of the request's row of the table, one a lane
-    const int rec_per_page = 1 << (a.log_page - 4);
-    auto issue = [&]() {
-      const int s = issued % kStages;
-      const int key0 = lc.k * kRecTokens;
-      bool load = key0 < lkeys;
-      int page = -1;
-      if (load) {
-        const int pi = key0 >> a.log_page;
-        if (lc.r != cache_r || pi < cache_p || pi >= cache_p + 32) {
-          cache_r = lc.r;
-          cache_p = pi;
-          const int last = (lc.req.kv - 1) >> a.log_page;
-          my_page = pi + lane <= last ? __ldg(a.table + static_cast<long long>(lc.r) * a.max_pages + pi + lane) : -1;
-        }
-        page = __shfl_sync(0xffffffffu, my_page, pi - cache_p);
-        load = page >= 0 && page < a.num_pages;
-        if (!load && lane == 0) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+    const int log_rec = a.log_page - 4;  // records of a page
+    const uint32_t page_bytes = static_cast<uint32_t>(a.Hkv) * kRecBytes << log_rec;
+    const uint8_t* head_base = a.pages + (static_cast<long long>(lc.h) * kRecBytes << log_rec);
+    uint32_t have_all = 0;  // two bits a stage: record i was loaded, or lies behind the last key
+    // page pi of the request at lc; false: not a page
+    auto find = [&](int pi, const uint8_t*& base) -> bool {
+      if (lc.r != cache_r || static_cast<unsigned>(pi - cache_p) >= 32u) {
+        cache_r = lc.r;
+        cache_p = pi;
+        const int last = (lc.req.kv - 1) >> a.log_page;
+        my_page = pi + lane <= last ? __ldg(a.table + static_cast<long long>(lc.r) * a.max_pages + pi + lane) : -1;
       }
-      if (lane == 0) {
-        sm.have[warp][s] = load;
-        if (load) {
-          const uint8_t* src =
-              a.pages + ((static_cast<long long>(page) * a.Hkv + lc.h) * rec_per_page + (lc.k & (rec_per_page - 1))) *
-                            kRecBytes;
-          mbar_arrive_expect_tx(&sm.full[warp][s], kRecBytes);
-          bulk_load(sm.ring[warp][s], src, kRecBytes, &sm.full[warp][s]);
+      const unsigned page = __shfl_sync(0xffffffffu, my_page, pi - cache_p);
+      if (page >= static_cast<unsigned>(a.num_pages)) {
+        if (lane == 0) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+        return false;
+      }
+      base = head_base + static_cast<unsigned long long>(page) * page_bytes;
+      return true;
+    };
+    auto issue = [&](int s) {
+      uint64_t* bar = &sm.full[warp][s];
+      uint8_t* dst = sm.ring[warp][s];
+      uint32_t have = 3;
+      const uint8_t *s0 = nullptr, *s1 = nullptr;
+      if (log_rec > 0) {
+        // both records lie in one page; the second may hold no key, but is there
+        if (lc.k * kUnit < lkeys) {
+          have = find(lc.k * 2 >> log_rec, s0) ? 3 : 0;
+          s0 += (lc.k * 2 & ((1 << log_rec) - 1)) * kRecBytes;
         } else {
-          mbar_arrive(&sm.full[warp][s]);
+          have = 4;
+        }
+        if (lane == 0) {
+          if (have == 3) {
+            mbar_arrive_expect_tx(bar, kUnitBytes);
+            bulk_load(dst, s0, kUnitBytes, bar);
+          } else {
+            mbar_arrive(bar);
+          }
+        }
+      } else {
+        const bool in0 = lc.k * kUnit < lkeys, in1 = lc.k * kUnit + kRecTokens < lkeys;
+        const bool ok0 = in0 && find(lc.k * 2, s0), ok1 = in1 && find(lc.k * 2 + 1, s1);
+        have = (ok0 || !in0 ? 1 : 0) | (ok1 || !in1 ? 2 : 0);
+        if (lane == 0) {
+          if (ok0 || ok1) {
+            mbar_arrive_expect_tx(bar, (ok0 ? kRecBytes : 0) + (ok1 ? kRecBytes : 0));
+            if (ok0) bulk_load(dst, s0, kRecBytes, bar);
+            if (ok1) bulk_load(dst + kRecBytes, s1, kRecBytes, bar);
+          } else {
+            mbar_arrive(bar);
+          }
         }
       }
+      have_all = (have_all & ~(3u << (2 * s))) | ((have & 3) << (2 * s));
       ++issued;
       if (issued < total && ++lc.k == lc.nu) {
         lc.next_item(a, share);
         lkeys = S::keys(a, lc.req, lc.j);
+        head_base = a.pages + (static_cast<long long>(lc.h) * kRecBytes << log_rec);
       }
     };
-    for (int i = 0; i < kStages && i < total; ++i) issue();
+    for (int i = 0; i < STAGES && i < total; ++i) issue(i);
 
     uint32_t qf[NT][16];
-    float rs[NT][2], m[NT][2], l[NT][2];
+    float rs[NT][2], m[NT][2], l[NT][2], base[NT][2];  // base: -m, or 0 where there is none yet
     int lim[NT][2];
     float acc[NT][8][4];
-    int lim_min = 0;
+    int lim_min = 0, seen = 0;
     bool from_start = false;
+    int s = 0;
+    uint32_t parity = 0;
 
     for (int i = 0; i < total; ++i) {
       if (i == 0 || cc.k == 0) {
@@ -208,6 +254,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         from_start = cc.k == 0;
         const int rows = cc.req.n * a.G;
         lim_min = visible(a, cc.req, cc.j * RT / a.G);
+        seen = S::keys(a, cc.req, cc.j);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int row = cc.j * RT + n * 8 + g;
@@ -246,33 +293,39 @@ __global__ void __launch_bounds__(W * 32, 1)
             const int r2 = cc.j * RT + n * 8 + 2 * c + e;
             lim[n][e] = visible(a, cc.req, min(r2, rows - 1) / a.G);
             m[n][e] = -INFINITY;
-            l[n][e] = 0.0f;
+            l[n][e] = base[n][e] = 0.0f;
           }
 #pragma unroll
           for (int x = 0; x < 8; ++x) acc[n][x][0] = acc[n][x][1] = acc[n][x][2] = acc[n][x][3] = 0.0f;
         }
       }
 
-      const int s = i % kStages;
-      ok = mbar_wait(&sm.full[warp][s], (i / kStages) & 1, &sm.abort, a.status, kTimeoutNs);
+      ok = mbar_wait(&sm.full[warp][s], parity, &sm.abort, a.status, kTimeoutNs);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      if (sm.have[warp][s]) {
-        const uint8_t* rec = sm.ring[warp][s];
-        const int key0 = cc.k * kRecTokens;
-        // ---- S^T = K Q^T: row x of the 16 keys is token 8 (x / 8) + 4 (x & 1) + ((x & 7) >> 1)
-        float sc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+      const uint32_t have = have_all >> (2 * s) & 3;
+      const int key0 = cc.k * kUnit;
+      if (key0 < seen) {
+        const uint8_t* unit = sm.ring[warp][s];
+        // ---- S^T = K Q^T: row x of a record's 16 keys is token 8 (x / 8) + 4 (x & 1) + ((x & 7) >> 1)
+        float sc[NT][2][4];
         const int ta = 4 * (g & 1) + (g >> 1);
-        {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* rec = unit + u * kRecBytes;
           const uint4 ka = *reinterpret_cast<const uint4*>(rec + ta * 64 + c * 16);
           const uint4 kb = *reinterpret_cast<const uint4*>(rec + (ta + 8) * 64 + c * 16);
           const uint32_t sa = from_e4m3x2(*reinterpret_cast<const uint16_t*>(rec + kRecKS + ta * 8 + 2 * c));
           const uint32_t sb = from_e4m3x2(*reinterpret_cast<const uint16_t*>(rec + kRecKS + (ta + 8) * 8 + 2 * c));
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          // two chains of products, joined below: half the wait for one
+          float even[NT][4], odd[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) even[n][e] = odd[n][e] = 0.0f;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const uint32_t s1 = x < 2 ? dup_lo(sa) : dup_hi(sa), s2 = x < 2 ? dup_lo(sb) : dup_hi(sb);
@@ -284,36 +337,46 @@ __global__ void __launch_bounds__(W * 32, 1)
               const uint32_t f[4] = {mul_f16x2(va[2 * y], s1), mul_f16x2(vb[2 * y], s2), mul_f16x2(va[2 * y + 1], s1),
                                      mul_f16x2(vb[2 * y + 1], s2)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(sc[n], f, qf[n][4 * x + 2 * y], qf[n][4 * x + 2 * y + 1]);
+              for (int n = 0; n < NT; ++n)
+                mma16816(y ? odd[n] : even[n], f, qf[n][4 * x + 2 * y], qf[n][4 * x + 2 * y + 1]);
             }
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][u][e] = even[n][e] + odd[n][e];
         }
-        // ---- softmax over the keys
+        // ---- softmax over the keys, in units of 1 / rs (a power of two times log2(e) / sqrt(D))
+        if (key0 + kUnit > lim_min || have != 3) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 16 * u + ta + 8 * (e >> 1) >= lim[n][e & 1] || !(have >> u & 1)) sc[n][u][e] = -INFINITY;
+        }
         bool grow = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] *= rs[n][e & 1];
-          if (key0 + kRecTokens > lim_min) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + ta + 8 * (e >> 1) >= lim[n][e & 1]) sc[n][e] = -INFINITY;
+          for (int e = 0; e < 2; ++e) {
+            const float t = fmaxf(max3f(sc[n][0][e], sc[n][0][e + 2], sc[n][1][e]), sc[n][1][e + 2]) * rs[n][e];
+            grow |= t > m[n][e] + 8.0f;
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) grow |= fmaxf(sc[n][e], sc[n][e + 2]) > m[n][e] + 8.0f;
-        }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float t = fmaxf(sc[n][e], sc[n][e + 2]);
+              float t = fmaxf(max3f(sc[n][0][e], sc[n][0][e + 2], sc[n][1][e]), sc[n][1][e + 2]) * rs[n][e];
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
               if (t > m[n][e] + 8.0f) {
-                const float alpha = part_weight(m[n][e], t);
+                const float alpha = ex2_approx(m[n][e] - t);  // 0 for the first maximum
                 m[n][e] = t;
+                base[n][e] = -t;
                 l[n][e] *= alpha;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
@@ -323,28 +386,30 @@ __global__ void __launch_bounds__(W * 32, 1)
               }
             }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[2][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float base = m[n][e] == -INFINITY ? 0.0f : m[n][e];
-            sc[n][e] = ex2_approx(sc[n][e] - base);
-            sc[n][e + 2] = ex2_approx(sc[n][e + 2] - base);
-            l[n][e] += sc[n][e] + sc[n][e + 2];
+          for (int n = 0; n < NT; ++n) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = ex2_approx(__fmaf_rn(sc[n][u][e], rs[n][e & 1], base[n][e & 1]));
+            l[n][0] += p[0] + p[2];
+            l[n][1] += p[1] + p[3];
+            pb[u][n][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+            pb[u][n][1] = transpose8x8(pack_f16x2(p[2], p[3]));
           }
-          pb[n][0] = transpose8x8(pack_f16x2(sc[n][0], sc[n][1]));
-          pb[n][1] = transpose8x8(pack_f16x2(sc[n][2], sc[n][3]));
-        }
         // ---- O^T += V^T P^T: thread (g, c) has channels 16 g .. 16 g + 15 of tokens c, c + 4, c + 8, c + 12
-        {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* rec = unit + u * kRecBytes;
           uint2 w[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const uint2*>(rec + kRecV + (c + 4 * x) * 64 + g * 8);
           uint32_t vs = *reinterpret_cast<const uint32_t*>(rec + kRecVS + g * 16 + c * 4);
-          if (key0 + kRecTokens > cc.req.kv) {
-            // nothing was stored behind the last token: its scales may be NaN
-            const int left = cc.req.kv - key0;
+          if (key0 + kUnit > seen || have != 3) {
+            // behind the last token, or in a record that was not loaded, the scales may be NaN
+            const int left = have >> u & 1 ? seen - key0 - 16 * u : 0;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               if (c + 4 * x >= left) vs &= ~(0xffu << (8 * x));
@@ -365,20 +430,24 @@ __global__ void __launch_bounds__(W * 32, 1)
               const uint32_t f[4] = {mul_f16x2(e01[x], s01), mul_f16x2(o01[x], s01), mul_f16x2(e23[x], s23),
                                      mul_f16x2(o23[x], s23)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(acc[n][4 * y + x], f, pb[n][0], pb[n][1]);
+              for (int n = 0; n < NT; ++n) mma16816(acc[n][4 * y + x], f, pb[u][n][0], pb[u][n][1]);
             }
           }
         }
       }
-      __syncwarp();  // the record has been read
-      if (issued < total) issue();
+      __syncwarp();  // the unit has been read
+      if (issued < total) issue(s);
+      if (++s == STAGES) {
+        s = 0;
+        parity ^= 1;
+      }
 
       const bool done = cc.k + 1 == cc.nu;
       if (done || i + 1 == total) {
         // ---- the item, or the warp's share of it, is complete: thread (g, c) holds channels 16 g .. of rows 2c, 2c + 1
         const int rows = cc.req.n * a.G - cc.j * RT;
         float* piece = reinterpret_cast<float*>(from_start ? sm.ring[warp][0] : sm.piece[warp]);
-        static_assert(Sm::kPieceBytes <= kStages * kRecBytes, "the last piece takes the place of the ring");
+        static_assert(Sm::kPieceBytes <= STAGES * kUnitBytes, "the last piece takes the place of the ring");
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -413,7 +482,7 @@ __global__ void __launch_bounds__(W * 32, 1)
             }
           }
         if (!(from_start && done) && lane == 0)
-          sm.meta[2 * warp + (from_start ? 1 : 0)] = PieceMeta{cc.item0, cc.nu, cc.r, cc.h, cc.j};
+          sm.meta[2 * warp + (from_start ? 1 : 0)] = PieceMeta{cc.item0, cc.nu, cc.h, cc.j, cc.req.q0, min(RT, rows)};
         if (i + 1 < total) cc.next_item(a, share);
       } else {
         ++cc.k;
@@ -421,54 +490,45 @@ __global__ void __launch_bounds__(W * 32, 1)
     }
     if (!ok) {
       // a wait ran out: every copy issued must land before the CTA's shared memory is released
-      for (int s = 0; s < kStages; ++s)
+      for (int s = 0; s < STAGES; ++s)
         if (issued > s) {
-          const int last = issued - 1 - ((issued - 1 - s) % kStages);
-          mbar_wait_drain(&sm.full[warp][s], (last / kStages) & 1, kTimeoutNs);
+          const int last = issued - 1 - ((issued - 1 - s) % STAGES);
+          mbar_wait_drain(&sm.full[warp][s], (last / STAGES) & 1, kTimeoutNs);
         }
     }
   }
   __syncthreads();
   if (sm.abort) return;
 
-  // ---- join the warps' pieces of each item, all warps over its rows
+  // ---- join the warps' pieces of each item, all warps over its rows; lane p looks after piece p
+  static_assert(2 * W <= 32, "one lane per piece");
   int* counters = static_cast<int*>(a.ws);
   float* parts = reinterpret_cast<float*>(counters + kMaxWorkers);
   constexpr size_t kPart = part_floats<RT>();
+  const long long key = lane < 2 * W ? sm.meta[lane].item0 : -1;
+  const float* mine_at = reinterpret_cast<const float*>(lane & 1 ? &sm.ring[lane / 2 % W][0][0] : &sm.piece[lane / 2 % W][0]);
+  const unsigned alike = __match_any_sync(0xffffffffu, key);
+  unsigned leaders = __ballot_sync(0xffffffffu, key >= 0 && __ffs(alike) - 1 == lane);
   PieceMeta cross[2];  // items that go beyond the CTA: begun before it, going on after it
   cross[0].item0 = cross[1].item0 = -1;
-  for (int p0 = 0; p0 < 2 * W;) {
-    const PieceMeta mt = sm.meta[p0];
-    if (mt.item0 < 0) {
-      ++p0;
-      continue;
-    }
-    int p1 = p0 + 1;
-    while (p1 < 2 * W && (sm.meta[p1].item0 < 0 || sm.meta[p1].item0 == mt.item0)) ++p1;
-    const Request req = load_request(a, mt.r, false);
-    const int rows = min(RT, req.n * a.G - mt.j * RT);
+  while (leaders) {
+    const int lead = __ffs(leaders) - 1;
+    leaders &= leaders - 1;
+    const unsigned group = __shfl_sync(0xffffffffu, alike, lead);
+    const PieceMeta mt = sm.meta[lead];
     const bool whole = mt.item0 >= cs && mt.item0 + mt.nu <= ce;
     const int slot = mt.item0 < cs ? 0 : 1;
     if (!whole) cross[slot] = mt;
-    for (int row = warp; row < rows; row += W) {
-      RowPart t;
-      t.m = -INFINITY;
-      t.l = 0.0f;
-      t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      auto piece_of = [&](int p) -> const float* {
-        return reinterpret_cast<const float*>(p & 1 ? &sm.ring[p >> 1][0][0] : &sm.piece[p >> 1][0]);
-      };
-      for (int p = p0; p < p1; ++p)
-        if (sm.meta[p].item0 >= 0) t.m = fmaxf(t.m, piece_of(p)[RT * 128 + row]);
-      for (int p = p0; p < p1; ++p)
-        if (sm.meta[p].item0 >= 0) {
-          const float* f = piece_of(p);
-          // a piece without a maximum has nothing but zeros, or the NaN of its scores
-          const float pm = f[RT * 128 + row], w = pm == -INFINITY ? 1.0f : part_weight(pm, t.m);
-          add_part(t, reinterpret_cast<const float4*>(f + row * 128)[lane], w, f[RT * 129 + row]);
-        }
+    for (int row = warp; row < mt.rows; row += W) {
+      const bool in = group >> lane & 1;
+      RowPart t = join_weights(in ? mine_at[RT * 128 + row] : -INFINITY, in ? mine_at[RT * 129 + row] : 0.0f);
+      for (unsigned left = group; left; left &= left - 1) {
+        const int p = __ffs(left) - 1;
+        const float* f = reinterpret_cast<const float*>(p & 1 ? &sm.ring[p >> 1][0][0] : &sm.piece[p >> 1][0]);
+        add_part(t, reinterpret_cast<const float4*>(f + row * 128)[lane], __shfl_sync(0xffffffffu, t.w, p));
+      }
       if (whole) {
-        write_row<F16>(a, req, mt.h, mt.j * RT + row, t);
+        write_row<F16>(a, mt, mt.j * RT + row, t);
       } else {
         float* f = parts + (static_cast<size_t>(cta) * 2 + slot) * kPart;
         reinterpret_cast<float4*>(f + row * 128)[lane] = t.o;
@@ -478,55 +538,59 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
       }
     }
-    p0 = p1;
   }
   if (cross[0].item0 < 0 && cross[1].item0 < 0) return;
 
   // ---- join the CTAs' parts: the last of an item's CTAs to arrive, in the order of the line
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int x = 0; x < 2; ++x)
-      if (cross[x].item0 >= 0) {
-        const int first = worker_of(U, cross[x].item0, N), last = worker_of(U, cross[x].item0 + cross[x].nu - 1, N);
-        if (atomicAdd(counters + first, 1) == last - first) {
-          counters[first] = 0;  // as the next call finds it
-          sm.join[x] = 1;
-        }
-      }
-    __threadfence();
+  if (threadIdx.x < 2 && cross[threadIdx.x].item0 >= 0) {
+    const PieceMeta& mt = threadIdx.x ? cross[1] : cross[0];
+    const int first = cut.worker_of(mt.item0), last = cut.worker_of(mt.item0 + mt.nu - 1);
+    __threadfence();  // the CTA's parts before the count
+    if (atomicAdd(counters + first, 1) == last - first) {
+      counters[first] = 0;  // as the next call finds it
+      __threadfence();
+      sm.join[threadIdx.x][0] = first;
+      sm.join[threadIdx.x][1] = last;
+    }
   }
   __syncthreads();
+#pragma unroll
   for (int x = 0; x < 2; ++x) {
-    if (!sm.join[x]) continue;
+    const int first = sm.join[x][0], last = sm.join[x][1];
+    if (first < 0) continue;
     const PieceMeta mt = cross[x];
-    const Request req = load_request(a, mt.r, false);
-    const int first = worker_of(U, mt.item0, N), last = worker_of(U, mt.item0 + mt.nu - 1, N);
-    const int rows = min(RT, req.n * a.G - mt.j * RT);
-    for (int row = warp; row < rows; row += W) {
+    for (int row = warp; row < mt.rows; row += W) {
       auto part_of = [&](int w) { return parts + (static_cast<size_t>(w) * 2 + (w == first ? 1 : 0)) * kPart; };
       RowPart t;
       t.m = -INFINITY;
       t.l = 0.0f;
       t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int w = first + lane; w <= last; w += 32) t.m = fmaxf(t.m, __ldcg(part_of(w) + RT * 128 + row));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) t.m = fmaxf(t.m, __shfl_xor_sync(0xffffffffu, t.m, d));
-#pragma unroll 4
-      for (int w = first; w <= last; ++w) {
-        const float* f = part_of(w);
-        const float pm = __ldcg(f + RT * 128 + row), pw = pm == -INFINITY ? 1.0f : part_weight(pm, t.m);
-        add_part(t, __ldcg(reinterpret_cast<const float4*>(f + row * 128) + lane), pw, __ldcg(f + RT * 129 + row));
+      for (int w0 = first; w0 <= last; w0 += 32) {
+        const bool in = w0 + lane <= last;
+        const float* f = part_of(in ? w0 + lane : last);
+        RowPart u = join_weights(in ? __ldcg(f + RT * 128 + row) : -INFINITY, in ? __ldcg(f + RT * 129 + row) : 0.0f);
+        const int n = min(32, last - w0 + 1);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i)
+          add_part(u, __ldcg(reinterpret_cast<const float4*>(part_of(w0 + i) + row * 128) + lane),
+                   __shfl_sync(0xffffffffu, u.w, i));
+        // the 32 parts' sum joins those before it
+        const float m = fmaxf(t.m, u.m), wt = part_weight(t.m, m), wu = part_weight(u.m, m);
+        t.o = make_float4(wt * t.o.x + wu * u.o.x, wt * t.o.y + wu * u.o.y, wt * t.o.z + wu * u.o.z,
+                          wt * t.o.w + wu * u.o.w);
+        t.l = wt * t.l + wu * u.l;
+        t.m = m;
       }
-      write_row<F16>(a, req, mt.h, mt.j * RT + row, t);
+      write_row<F16>(a, mt, mt.j * RT + row, t);
     }
   }
 }
 
-template <int NT, int W>
+template <int NT, int W, int STAGES>
 cudaError_t launch_small(const AttnArgs& a, const Share& share, bool f16, int num_sms, cudaStream_t stream) {
-  auto kern = f16 ? cache_attn_small_kernel<NT, true, W> : cache_attn_small_kernel<NT, false, W>;
-  constexpr int smem = static_cast<int>(sizeof(Smem<NT, W>));
+  auto kern = f16 ? cache_attn_small_kernel<NT, true, W, STAGES> : cache_attn_small_kernel<NT, false, W, STAGES>;
+  constexpr int smem = static_cast<int>(sizeof(Smem<NT, W, STAGES>));
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -543,8 +607,8 @@ size_t cache_attn_small_workspace(int num_workers) {
 cudaError_t launch_cache_attn_small(const cache::AttnArgs& a, int over, int upto, bool f16, int rows, int num_sms,
                                     cudaStream_t stream) {
   const Share share{over, upto};
-  return rows <= 8 ? launch_small<1, 16>(a, share, f16, num_sms, stream)
-                   : launch_small<2, 12>(a, share, f16, num_sms, stream);
+  return rows <= 8 ? launch_small<1, 12, 3>(a, share, f16, num_sms, stream)
+                   : launch_small<2, 8, 4>(a, share, f16, num_sms, stream);
 }
 
 }  // namespace vsa

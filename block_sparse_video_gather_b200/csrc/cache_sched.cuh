@@ -5,8 +5,8 @@
 // of RT rows; an item is one (request, key head, tile).  Its cached tokens, as
 // far as the tile's last row sees them, are cut into units of KT keys (an item
 // that sees nothing has one unit, which writes its rows).  All units of the
-// batch in item order form one line, and worker i of N takes [U i / N, U (i + 1)
-// / N): lengths as uneven as they may be, each worker reads the same amount to
+// batch in item order form one line, and each of N workers takes U / N of them,
+// the first U % N one more: lengths as uneven as they may be, each worker reads the same amount to
 // within a unit.  Items that end up in several workers are joined by their
 // running maxima and sums.  Every worker finds its place by itself from cu and
 // kv_len, so lengths stay on the device and a captured call takes new ones.
@@ -34,6 +34,12 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
     a = t;
   }
   return s;
+}
+
+// a / b for a >= 0, b > 0, in 32 bits where both fit.
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+  if ((a | b) >> 32 == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
 }
 
 template <int RT, int KT>
@@ -72,26 +78,70 @@ __device__ __forceinline__ bool takes(const Share& s, const AttnArgs& a, const R
   return rows > s.over && rows <= s.upto;
 }
 
-// Units of each request, summed: pre[r] = units of requests 0 .. r-1, pre[R] = U.
-// All threads of the CTA; ends with a barrier.
-template <class S, int THREADS>
-__device__ __forceinline__ void scan_units(const AttnArgs& a, const Share& share, long long* pre, long long* part) {
-  const int per = (a.R + THREADS - 1) / THREADS;
-  const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
-  const bool report = blockIdx.x == 0;
-  long long sum = 0;
-  for (int r = r0; r < r1; ++r) {
-    const Request q = load_request(a, r, report);
-    pre[r] = sum;
-    if (takes(share, a, q)) sum += S::units_before(a, q, S::tiles(a, q)) * a.Hkv;
+// Where each request's units begin in the line.  Up to 32 requests: lane r of
+// every warp holds request r's, and nothing goes through shared memory; more:
+// one array of sums in shared memory, made by the whole CTA.
+struct Line {
+  long long total;     // U
+  long long at, units; // lane r: first unit and units of request r (R <= 32)
+  const long long* pre;  // [R + 1] first units (R > 32)
+
+  // The request that holds unit u < U, and its first unit.  All lanes of a warp.
+  __device__ __forceinline__ int request_of(int R, long long u, long long& first) const {
+    if (R <= 32) {
+      const int lane = threadIdx.x & 31;
+      const int r = __ffs(__ballot_sync(0xffffffffu, lane < R && u >= at && u < at + units)) - 1;
+      first = __shfl_sync(0xffffffffu, at, r);
+      return r;
+    }
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    first = pre[lo];
+    return lo;
   }
-  long long v = sum;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+};
+
+__device__ __forceinline__ long long warp_scan(long long v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long u = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v += u;
   }
+  return v;
+}
+
+// All threads of the CTA; `pre` [R + 1] and `part` [warps] in shared memory are
+// used for more than 32 requests only, and then the call ends with a barrier.
+template <class S, int THREADS>
+__device__ __forceinline__ Line make_line(const AttnArgs& a, const Share& share, long long* pre, long long* part) {
+  Line line;
+  line.pre = pre;
+  line.at = line.units = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto units_of = [&](int r, bool report) -> long long {
+    const Request q = load_request(a, r, report);
+    return takes(share, a, q) ? S::units_before(a, q, S::tiles(a, q)) * a.Hkv : 0;
+  };
+  if (a.R <= 32) {
+    if (lane < a.R) line.units = units_of(lane, blockIdx.x == 0 && warp == 0);
+    const long long v = warp_scan(line.units);
+    line.at = v - line.units;
+    line.total = __shfl_sync(0xffffffffu, v, 31);
+    return line;
+  }
+  const int per = (a.R + THREADS - 1) / THREADS;
+  const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
+  long long sum = 0;
+  for (int r = r0; r < r1; ++r) {
+    pre[r] = sum;
+    sum += units_of(r, blockIdx.x == 0);
+  }
+  const long long v = warp_scan(sum);
   if (lane == 31) part[warp] = v;
   __syncthreads();
   long long before = v - sum;
@@ -99,6 +149,8 @@ __device__ __forceinline__ void scan_units(const AttnArgs& a, const Share& share
   for (int r = r0; r < r1; ++r) pre[r] += before;
   if (threadIdx.x == THREADS - 1) pre[a.R] = before + sum;
   __syncthreads();
+  line.total = pre[a.R];
+  return line;
 }
 
 // A place in the line of units.
@@ -110,20 +162,15 @@ struct Cursor {
   Request req;
   long long item0;     // the item's first unit in the line
 
-  // Unit u of the line; pre from scan_units.
-  __device__ __forceinline__ void seek(const AttnArgs& a, const long long* pre, long long u) {
-    int lo = 0, hi = a.R;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    r = lo;
+  // Unit u of the line.  All lanes of a warp.
+  __device__ __forceinline__ void seek(const AttnArgs& a, const Line& line, long long u) {
+    long long first;
+    r = line.request_of(a.R, u, first);
     req = load_request(a, r, false);
     nt = S::tiles(a, req);
     const long long head = S::units_before(a, req, nt);
-    long long rem = u - pre[r];
-    h = static_cast<int>(rem / head);
+    long long rem = u - first;
+    h = static_cast<int>(div_small(rem, head));
     rem -= h * head;
     int tl = 0, th = nt;
     while (th - tl > 1) {
@@ -155,11 +202,20 @@ struct Cursor {
   }
 };
 
-// Worker i of n over U units; and the worker that holds unit u.
-__device__ __forceinline__ long long range_start(long long U, int i, int n) { return U * i / n; }
-__device__ __forceinline__ int worker_of(long long U, long long u, int n) {
-  return static_cast<int>(((u + 1) * n - 1) / U);
-}
+// The line cut for n workers: the first U % n get one unit more than the others.
+struct Cut {
+  long long size, more;  // U / n, U % n
+  __device__ __forceinline__ Cut(long long U, int n) {
+    size = div_small(U, n);
+    more = U - size * n;
+  }
+  __device__ __forceinline__ long long start(int i) const { return i * size + min(static_cast<long long>(i), more); }
+  // The worker that holds unit u.
+  __device__ __forceinline__ int worker_of(long long u) const {
+    const long long big = more * (size + 1);
+    return static_cast<int>(u < big ? div_small(u, size + 1) : more + div_small(u - big, size));
+  }
+};
 
 // Workspace: counters of joined items, then the workers' parts.  A worker's
 // range cuts at most two items, its first (slot 0) and the one that starts in
