@@ -1,0 +1,676 @@
+// cache_attn_chunk.cu -- attention over the 4-bit cache for many rows a
+// request: a chunk of a video or a piece of a prompt, on the tensor cores
+// (tcgen05, accumulators in tensor memory).
+//
+// Work: the line of (request, key head, 256-row tile) x 128-key units of
+// cache_sched.cuh, cut evenly over one persistent CTA per SM.  The pipeline is
+// the fine stage's (attn_fwd.cu): two 128-row query tiles, S and P in the same
+// tensor memory, PV(t) and S(t + 1) of one tile under the softmax of the other.
+// What differs is where the operands come from.  Q is read by the softmax
+// threads, a row each, which bring it to fp16 (bf16: times a power of two per
+// row, so that nothing is lost; cache_attn_small.cu) and write the swizzled
+// tile that TMA would have; K and V are made from codes by a warpgroup of their
+// own, which loads the words of a 128-key tile one tile ahead into registers,
+// converts them (code * scale, exact in fp16) and writes the same tiles.
+//
+// Warp roles (512 threads):
+//   warp 0       tensor-memory owner and MMA issuer
+//   warp 1       walks the CTA's share of the line and hands its segments (an
+//                item's units, or part of them) to the others through a ring in
+//                shared memory, so that their registers hold no schedule
+//                (warps 2 and 3 idle)
+//   warps 4-7    K and V tiles from codes: a thread 32 channels of 4 keys
+//   warps 8-11   rows of query tile 0: Q, softmax, output
+//   warps 12-15  rows of query tile 1
+// Bound: the tensor pipe where there are enough keys, as in the fine stage;
+// the conversion (256 values a key and CTA, whatever its rows) runs beside it.
+//
+// An item cut between CTAs leaves its rows' sums, maxima and denominators in
+// the workspace, and a second kernel joins them in the order of the line.
+// Every mbarrier wait is bounded, as in the fine stage.
+#include <cuda_fp16.h>
+
+#include "cache.cuh"
+#include "cache_kernels.h"
+#include "cache_sched.cuh"
+
+namespace vsa {
+
+namespace {
+
+using namespace cache;
+
+constexpr int kThreads = 512;
+constexpr int kRowTile = 256, kKeyTile = 128;
+constexpr int kStagesK = 3, kStagesV = 2, kSegs = 4;
+constexpr uint32_t kHalfBytes = 128 * 128;       // 128 rows x 64 fp16 (one 128-B swizzle column)
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // 128 rows x 128 fp16
+constexpr uint32_t kSmemQ = 0;
+constexpr uint32_t kSmemK = kSmemQ + 2 * kTileBytes;
+constexpr uint32_t kSmemV = kSmemK + kStagesK * kTileBytes;
+constexpr uint32_t kSmemBar = kSmemV + kStagesV * kTileBytes;
+constexpr uint32_t kSmemTotal = kSmemBar + 512 + 1024;  // barriers, segments + 1 KB alignment slack
+constexpr uint64_t kTimeoutNs = 2000000000ull;          // 2 s per wait
+// Register split: launched at 128 per thread; 128 x (72 + 88) + 256 x 176 = 512 x 128.
+constexpr int kRegsMma = 72, kRegsLoad = 88, kRegsRows = 176;
+static_assert(128 * (kRegsMma + kRegsLoad) + 256 * kRegsRows == kThreads * 128, "register split must match the launch");
+
+using S = Sched<kRowTile, kKeyTile>;
+
+// Units [k0, k0 + n) of an item; n = 0: the end.
+struct Seg {
+  int r, h, j;        // request, key head, row tile
+  int k0, n;
+  int whole;          // the whole item
+  int q0, tokens, kv; // the request
+  int last;           // an item that starts here and goes on after the CTA's share: the CTA of its last unit; else -1
+};
+
+struct Barriers {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kStagesK], k_empty[kStagesK];
+  uint64_t v_full[kStagesV], v_empty[kStagesV];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  Seg seg[kSegs];
+};
+static_assert(sizeof(Barriers) <= 512, "barrier block too large");
+constexpr int kSegReaders = 13;  // warps: the MMA issuer, 4 of the tiles, 8 of the rows
+
+// What the join kernel needs of an item that starts in a CTA's range and goes
+// on after it: in the workspace, one per CTA; last < 0: none.
+struct Joint {
+  int last;  // the CTA that holds the item's last unit
+  int h, j, q0, rows;
+  int pad[3];
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Barriers* bars, unsigned int* status) {
+  const bool ok = mbar_wait(bar, parity, &bars->abort, status, kTimeoutNs);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float* parts_of(void* ws, int workers) {
+  return reinterpret_cast<float*>(static_cast<Joint*>(ws) + workers);
+}
+
+// The next segment, for a warp; n = 0 at the end or when a wait ran out.
+struct SegReader {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ Seg next(Barriers* bars, unsigned int* status) {
+    Seg seg;
+    seg.n = 0;
+    if (!warp_wait(&bars->seg_full[at], parity, bars, status)) return seg;
+    seg = bars->seg[at];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->seg_empty[at]);
+    if (++at == kSegs) {
+      at = 0;
+      parity ^= 1;
+    }
+    return seg;
+  }
+};
+
+// 16 channels of a key, code times scale, as two 16-byte chunks of a tile.
+__device__ __forceinline__ void put_chunk(uint8_t* dst, uint32_t word, uint32_t scale) {
+  uint32_t v[4];
+  from_e2m1x8(word, v);
+  *reinterpret_cast<uint4*>(dst) =
+      make_uint4(mul_f16x2(v[0], scale), mul_f16x2(v[1], scale), mul_f16x2(v[2], scale), mul_f16x2(v[3], scale));
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attn_chunk_kernel(const __grid_constant__ AttnArgs a, const Share share) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + kSmemQ;
+  uint8_t* sK = smem + kSmemK;
+  uint8_t* sV = smem + kSmemV;
+  Barriers* bars = reinterpret_cast<Barriers*>(smem + kSmemBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, N = gridDim.x;
+
+  // the sums over many requests use the K ring before anything else does
+  const Line line = make_line<S, kThreads>(a, share, reinterpret_cast<long long*>(sK),
+                                           reinterpret_cast<long long*>(sQ));
+  const long long U = line.total;
+  Joint* joint = static_cast<Joint*>(a.ws) + cta;
+  if (threadIdx.x == 0) joint->last = -1;
+  const Cut cut(U, N);
+  const long long cs = cut.start(cta), ce = cut.start(cta + 1);
+  if (cs == ce) return;
+  Cursor<S> cur;
+  if (warp == 1) cur.seek(a, line, cs);
+  __syncthreads();
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 256);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < kStagesK; ++s) {
+      mbar_init(&bars->k_full[s], 128);
+      mbar_init(&bars->k_empty[s], 1);
+    }
+    for (int s = 0; s < kStagesV; ++s) {
+      mbar_init(&bars->v_full[s], 128);
+      mbar_init(&bars->v_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->o_full[i], 1);
+      mbar_init(&bars->o_empty[i], 128);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bars->seg_full[i], 1);
+      mbar_init(&bars->seg_empty[i], kSegReaders);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < 4) {
+    regs_dec<kRegsMma>();
+    if (warp == 1) {
+      // ------------------------------------------------------------ the CTA's segments
+      int at = 0;
+      uint32_t parity = 1;
+      int left = static_cast<int>(ce - cs);
+      while (true) {
+        const int n = min(left, cur.nu - cur.k);
+        if (!warp_wait(&bars->seg_empty[at], parity, bars, a.status)) break;
+        if (lane == 0) {
+          Seg g;
+          g.r = cur.r, g.h = cur.h, g.j = cur.j;
+          g.k0 = cur.k, g.n = n;
+          g.whole = n == cur.nu;
+          g.q0 = cur.req.q0, g.tokens = cur.req.n, g.kv = cur.req.kv;
+          g.last = cur.k == 0 && n < cur.nu ? cut.worker_of(cur.item0 + cur.nu - 1) : -1;
+          bars->seg[at] = g;
+          mbar_arrive(&bars->seg_full[at]);
+        }
+        __syncwarp();
+        if (n == 0) break;  // the end has been handed on
+        if (++at == kSegs) {
+          at = 0;
+          parity ^= 1;
+        }
+        left -= n;
+        if (left > 0) cur.next_item(a, share);
+      }
+    } else if (warp == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
+      constexpr uint64_t kTileDesc = kTileBytes >> 4;
+      constexpr uint32_t kIdescS = idesc_f16_f32(128, 128, 0, 0), kIdescPV = idesc_f16_f32(128, 128, 0, 1);
+      int sk = 0, sv = 0;                // ring places
+      uint32_t pk = 0, pv = 0;           // and their parities
+      uint32_t pq = 0, pp[2] = {0, 0}, po[2] = {1, 1};
+      bool ok = true;
+      auto issue_s = [&](int i) {
+        const uint32_t d = tmem + i * 128;
+        const uint64_t qa = dq0 + i * kTileDesc, b = dk0 + sk * kTileDesc;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+          mma_ss_w(d, qa + off, b + off, kIdescS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_w(&bars->s_full[i]);
+      };
+      auto issue_pv = [&](int i, bool acc) {
+        const uint32_t d = tmem + 256 + i * 128, pa = tmem + i * 128;
+        const uint64_t b = dv0 + sv * kTileDesc;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_w(d, pa + kk * 8, b + kk * (2048 >> 4), kIdescPV, (acc || kk > 0) ? 1u : 0u);
+      };
+      auto k_done = [&]() {
+        mma_commit_w(&bars->k_empty[sk]);
+        if (++sk == kStagesK) {
+          sk = 0;
+          pk ^= 1;
+        }
+      };
+      SegReader segs;
+      while (ok) {
+        const Seg cur = segs.next(bars, a.status);
+        const int n = cur.n;
+        if (n == 0) break;
+        const int tiles = cur.tokens * a.G - cur.j * kRowTile > 128 ? 2 : 1;
+        if (!(ok = warp_wait(&bars->q_full, pq, bars, a.status))) break;
+        pq ^= 1;
+        if (!(ok = warp_wait(&bars->k_full[sk], pk, bars, a.status))) break;
+        tc_fence_after();
+        issue_s(0);
+        if (tiles == 2) issue_s(1);
+        k_done();
+        for (int t = 0; t < n; ++t) {
+          const bool more = t + 1 < n;
+          if (!(ok = warp_wait(&bars->v_full[sv], pv, bars, a.status))) break;
+          if (!(ok = warp_wait(&bars->p_full[0], pp[0], bars, a.status))) break;
+          pp[0] ^= 1;
+          if (t == 0) {
+            if (!(ok = warp_wait(&bars->o_empty[0], po[0], bars, a.status))) break;
+            po[0] ^= 1;
+          }
+          tc_fence_after();
+          issue_pv(0, t > 0);
+          if (!more) mma_commit_w(&bars->o_full[0]);
+          if (more) {
+            if (!(ok = warp_wait(&bars->k_full[sk], pk, bars, a.status))) break;
+            tc_fence_after();
+            issue_s(0);
+          }
+          if (tiles == 2) {
+            if (!(ok = warp_wait(&bars->p_full[1], pp[1], bars, a.status))) break;
+            pp[1] ^= 1;
+            if (t == 0) {
+              if (!(ok = warp_wait(&bars->o_empty[1], po[1], bars, a.status))) break;
+              po[1] ^= 1;
+            }
+            tc_fence_after();
+            issue_pv(1, t > 0);
+          }
+          mma_commit_w(&bars->v_empty[sv]);
+          if (++sv == kStagesV) {
+            sv = 0;
+            pv ^= 1;
+          }
+          if (tiles == 2 && !more) mma_commit_w(&bars->o_full[1]);
+          if (more) {
+            if (tiles == 2) issue_s(1);
+            k_done();
+          }
+        }
+        if (!ok) break;
+        mma_commit_w(&bars->q_empty);
+      }
+      // Drain: wait for every MMA issued by this thread before TMEM and smem go away.
+      mma_commit_w(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0, kTimeoutNs);
+    }
+  } else if (warp < 8) {
+    regs_dec<kRegsLoad>();
+    // ------------------------------------------------------------ K and V tiles from codes
+    // Lane (g, c) of warp w: channels 32 c .. 32 c + 31 of keys 32 w + 8 x + g, x = 0 .. 3 (records 2 w and
+    // 2 w + 1 of the tile).  Its four 16-byte chunks of a key go to places (4 (c & 1) + y) ^ (key & 7) of half
+    // c >> 1; lanes of the upper half take y ^ 2 first, so that eight lanes always write eight different places.
+    const int w = warp - 4, g = lane >> 2, c = lane & 3;
+    const int log_rec = a.log_page - 4;
+    const unsigned page_bytes = static_cast<unsigned>(a.Hkv) * kRecBytes << log_rec;
+    uint32_t kw[16], vw[16], ks[4], vs[4];
+    int live = 0;  // keys of the record pair that hold a token, from 0; bad pages hold none
+    const uint8_t* rec[2];
+    auto place = [&](const Seg& cu, int t) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = t * 8 + w * 2 + x;  // record of the request
+        rec[x] = nullptr;
+        if (r * kRecTokens < cu.kv) {
+          const unsigned page =
+              __ldg(a.table + static_cast<long long>(cu.r) * a.max_pages + (r >> log_rec));
+          if (page < static_cast<unsigned>(a.num_pages))
+            rec[x] = a.pages + static_cast<unsigned long long>(page) * page_bytes +
+                     ((static_cast<long long>(cu.h) << log_rec) + (r & ((1 << log_rec) - 1))) * kRecBytes;
+          else if (lane == 0)
+            atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+        }
+      }
+      live = cu.kv - (t * kKeyTile + w * 32);
+    };
+    auto load_k = [&]() {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint8_t* p = rec[x >> 1];
+        const int tok = (x & 1) * 8 + g;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        ks[x] = 0;
+        if (p != nullptr && (x * 8 + g) < live) {
+          v = __ldg(reinterpret_cast<const uint4*>(p + tok * 64 + c * 16));
+          ks[x] = __ldg(reinterpret_cast<const uint16_t*>(p + kRecKS + tok * 8 + 2 * c));
+        }
+        kw[4 * x] = v.x, kw[4 * x + 1] = v.y, kw[4 * x + 2] = v.z, kw[4 * x + 3] = v.w;
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint8_t* p = rec[x >> 1];
+        const int tok = (x & 1) * 8 + g;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        vs[x] = 0;
+        if (p != nullptr && (x * 8 + g) < live) {
+          v = __ldg(reinterpret_cast<const uint4*>(p + kRecV + tok * 64 + c * 16));
+          const uint8_t* sp = p + kRecVS + 2 * c * 16 + (tok & 3) * 4 + (tok >> 2);
+          vs[x] = static_cast<uint32_t>(__ldg(sp)) | static_cast<uint32_t>(__ldg(sp + 16)) << 8;
+        }
+        vw[4 * x] = v.x, vw[4 * x + 1] = v.y, vw[4 * x + 2] = v.z, vw[4 * x + 3] = v.w;
+      }
+    };
+    auto store = [&](uint8_t* tile, const uint32_t (&word)[16], const uint32_t (&sc)[4]) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int key = w * 32 + x * 8 + g;
+        uint8_t* row = tile + (c >> 1) * kHalfBytes + key * 128;
+        const uint32_t s2 = from_e4m3x2(sc[x]), s_lo = dup_lo(s2), s_hi = dup_hi(s2);
+        const bool up = c >> 1;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int z = up ? y ^ 2 : y;
+          put_chunk(row + (((4 * (c & 1) + z) ^ (key & 7)) << 4), up ? word[4 * x + (y ^ 2)] : word[4 * x + y],
+                    z < 2 ? s_lo : s_hi);
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    int sk = 0, sv = 0;
+    uint32_t pk = 1, pv = 1;
+    bool ok = true;
+    SegReader segs;
+    Seg cur = segs.next(bars, a.status);
+    int t = 0;
+    if (cur.n > 0) {
+      place(cur, cur.k0);
+      load_k();
+    }
+    while (cur.n > 0 && ok) {
+      load_v();
+      if (!(ok = warp_wait(&bars->k_empty[sk], pk, bars, a.status))) break;
+      store(sK + sk * kTileBytes, kw, ks);
+      mbar_arrive(&bars->k_full[sk]);
+      if (++sk == kStagesK) {
+        sk = 0;
+        pk ^= 1;
+      }
+      if (++t == cur.n) {
+        t = 0;
+        cur = segs.next(bars, a.status);
+      }
+      if (cur.n > 0) {
+        place(cur, cur.k0 + t);
+        load_k();
+      }
+      if (!(ok = warp_wait(&bars->v_empty[sv], pv, bars, a.status))) break;
+      store(sV + sv * kTileBytes, vw, vs);
+      mbar_arrive(&bars->v_full[sv]);
+      if (++sv == kStagesV) {
+        sv = 0;
+        pv ^= 1;
+      }
+    }
+  } else {
+    regs_inc<kRegsRows>();
+    // ------------------------------------------------------------ Q, softmax and output, one thread per row
+    const int wg = (warp - 8) >> 2;
+    const int quarter = warp & 3;  // tensor-memory lane quarter of this warp
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + wg * 128;
+    const uint32_t tO = tmem + lane_off + 256 + wg * 128;
+    const int log_rec = a.log_page - 4;
+    uint32_t ps = 0, po = 0, pq = 1;
+    bool ok = true;
+    SegReader segs;
+    while (ok) {
+      const Seg cur = segs.next(bars, a.status);
+      const int n = cur.n;
+      if (n == 0) break;
+      const int rows = cur.tokens * a.G - cur.j * kRowTile;  // of the item, from this tile on
+      const bool active = wg == 0 || rows > 128;
+      const int row = wg * 128 + r;
+      const bool real = row < rows;
+      const int rr = cur.j * kRowTile + (real ? row : 0);
+      const int token = rr / a.G;
+      const int head = cur.h * a.G + (rr - token * a.G);
+      const long long dst = (static_cast<long long>(cur.q0) + token) * a.Hq + head;
+      const int lim = visible(a, Request{cur.q0, cur.tokens, cur.kv}, token);
+
+      // ---- Q row -> fp16, swizzled; the row's scale goes into the softmax
+      float inv = 1.0f;
+      if (!(ok = warp_wait(&bars->q_empty, pq, bars, a.status))) break;
+      pq ^= 1;
+      if (active) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(a.q + (static_cast<long long>(cur.q0) + token) * a.q_stride + head * 128);
+        uint32_t qw[64];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (real) v = __ldg(src + x);
+          qw[4 * x] = v.x, qw[4 * x + 1] = v.y, qw[4 * x + 2] = v.z, qw[4 * x + 3] = v.w;
+        }
+        if (!F16) {
+          float amax = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 64; ++x) amax = max3f(amax, fabsf(bf16_lo(qw[x])), fabsf(bf16_hi(qw[x])));
+          const int e = __float_as_uint(amax) >> 23;
+          const int upb = amax == 0.0f || e == 255 ? 0 : min(141 - e, 100);  // 2^upb * amax in [2^14, 2^15)
+          const float f = __uint_as_float((upb + 127) << 23);
+          inv = __uint_as_float((127 - upb) << 23);
+#pragma unroll
+          for (int x = 0; x < 64; ++x) qw[x] = pack_f16x2(bf16_lo(qw[x]) * f, bf16_hi(qw[x]) * f);
+        }
+        uint8_t* q_row = sQ + wg * kTileBytes + r * 128;
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          *reinterpret_cast<uint4*>(q_row + (x >> 3) * kHalfBytes + (((x & 7) ^ (r & 7)) << 4)) =
+              make_uint4(qw[4 * x], qw[4 * x + 1], qw[4 * x + 2], qw[4 * x + 3]);
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(&bars->q_full);
+      const float sl2 = a.scale_log2 * inv;
+
+      float m_used = -INFINITY, l = 0.0f;
+      for (int t = 0; t < n && active; ++t) {
+        const int key0 = (cur.k0 + t) * kKeyTile;
+        // pages of the tile's eight records, one a lane
+        bool bad = false;
+        if (lane < 8 && key0 + lane * kRecTokens < cur.kv) {
+          const unsigned page = __ldg(a.table + static_cast<long long>(cur.r) * a.max_pages +
+                                      (((key0 >> 4) + lane) >> log_rec));
+          bad = page >= static_cast<unsigned>(a.num_pages);
+        }
+        const unsigned bad_recs = __ballot_sync(0xffffffffu, bad);
+        if (!(ok = warp_wait(&bars->s_full[wg], ps, bars, a.status))) break;
+        ps ^= 1;
+        tc_fence_after();
+        float alpha = 1.0f;
+        bool rescale = false;
+        {
+          uint32_t sv[128];
+          tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+          tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
+          tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
+          tmem_wait_ld();
+          const int see = lim - key0;  // columns this row sees
+          if (see < kKeyTile || bad_recs) {
+#pragma unroll
+            for (int x = 0; x < 128; ++x)
+              if (x >= see || (bad_recs >> (x >> 4) & 1)) sv[x] = 0xff800000u;
+          }
+          float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 128; x += 8) {
+            a0 = max3f(a0, __uint_as_float(sv[x + 0]), __uint_as_float(sv[x + 1]));
+            a1 = max3f(a1, __uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3]));
+            a2 = max3f(a2, __uint_as_float(sv[x + 4]), __uint_as_float(sv[x + 5]));
+            a3 = max3f(a3, __uint_as_float(sv[x + 6]), __uint_as_float(sv[x + 7]));
+          }
+          const float mt = max3f(a0, a1, fmaxf(a2, a3)) * sl2;
+          const bool grow = mt > m_used + 8.0f;
+          rescale = grow && t > 0 && m_used != -INFINITY;
+          alpha = rescale ? ex2_approx(m_used - mt) : 1.0f;
+          if (grow) m_used = mt;
+          const float msub = (m_used == -INFINITY) ? 0.0f : m_used;
+          const uint64_t c2 = f2pack(sl2, sl2), nm2 = f2pack(-msub, -msub);
+          uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint64_t x = fma2(u2pack(sv[64 * hf + 2 * j], sv[64 * hf + 2 * j + 1]), c2, nm2);
+              float xa, xb;
+              f2unpack(x, xa, xb);
+              const float p0 = ex2_approx(xa), p1 = ex2_approx(xb);
+              pk[j] = pack_f16x2(p0, p1);
+              acc[j & 3] = add2(acc[j & 3], f2pack(p0, p1));
+            }
+            tmem_st32(tS + 32 * hf, pk);
+          }
+          float s0, s1, s2, s3, s4, s5, s6, s7;
+          f2unpack(acc[0], s0, s1);
+          f2unpack(acc[1], s2, s3);
+          f2unpack(acc[2], s4, s5);
+          f2unpack(acc[3], s6, s7);
+          l = l * alpha + (((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7)));
+        }
+        // Rescale this row of O when its maximum moved.  PV(t-1) is complete: the s_full commit just waited on
+        // follows it in issue order.
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t ov[32];
+            tmem_ld32(tO + x * 32, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+            tmem_st32(tO + x * 32, ov);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[wg]);
+      }
+      if (!ok) break;
+      if (active) {
+        if (!(ok = warp_wait(&bars->o_full[wg], po, bars, a.status))) break;
+        po ^= 1;
+        tc_fence_after();
+        if (cur.whole) {
+          const float scale = l != 0.0f ? 1.0f / l : 0.0f;
+          uint4* orow = reinterpret_cast<uint4*>(a.o + dst * 128);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t ov[32];
+            tmem_ld32(tO + x * 32, ov);
+            tmem_wait_ld();
+            uint4 o4[4];
+            uint32_t* wp = reinterpret_cast<uint32_t*>(o4);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              wp[j] = pack_half2<F16>(__uint_as_float(ov[2 * j]) * scale, __uint_as_float(ov[2 * j + 1]) * scale);
+            if (real) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) orow[x * 4 + j] = o4[j];
+            }
+          }
+          if (real) a.lse[dst] = l != 0.0f ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* part = parts_of(a.ws, N) + (static_cast<size_t>(cta) * 2 + (cur.k0 > 0 ? 0 : 1)) * part_floats<kRowTile>();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t ov[32];
+            tmem_ld32(tO + x * 32, ov);
+            tmem_wait_ld();
+            if (real) {
+              uint4* out = reinterpret_cast<uint4*>(part + row * 128 + x * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) out[j] = make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
+            }
+          }
+          if (real) {
+            part[kRowTile * 128 + row] = m_used;
+            part[kRowTile * 129 + row] = l;
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->o_empty[wg]);
+      }
+      if (wg == 0 && r == 0 && cur.last >= 0) *joint = Joint{cur.last, cur.h, cur.j, cur.q0, min(kRowTile, rows), {0, 0, 0}};
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the rows of the items that more than one CTA worked on: a warp per row.
+constexpr int kJoinRows = 8;
+template <bool F16>
+__global__ void __launch_bounds__(kJoinRows * 32)
+    cache_attn_join_kernel(const __grid_constant__ AttnArgs a, int workers) {
+  const int first = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const Joint jt = static_cast<const Joint*>(a.ws)[first];
+  if (jt.last < 0 || row >= jt.rows) return;
+  constexpr size_t kPart = part_floats<kRowTile>();
+  const float* parts = parts_of(a.ws, workers);
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int w = first; w <= jt.last; ++w) {
+    const float* f = parts + (static_cast<size_t>(w) * 2 + (w == first ? 1 : 0)) * kPart;
+    const float4 po = reinterpret_cast<const float4*>(f + row * 128)[lane];
+    const float pm = f[kRowTile * 128 + row], pl = f[kRowTile * 129 + row];
+    const float mn = fmaxf(m, pm);
+    // without a maximum a part has nothing but zeros, or the NaN of its scores
+    const float w0 = m == -INFINITY ? 1.0f : ex2_approx(m - mn), w1 = pm == -INFINITY ? 1.0f : ex2_approx(pm - mn);
+    o = make_float4(w0 * o.x + w1 * po.x, w0 * o.y + w1 * po.y, w0 * o.z + w1 * po.z, w0 * o.w + w1 * po.w);
+    l = w0 * l + w1 * pl;
+    m = mn;
+  }
+  const int rr = jt.j * kRowTile + row, token = rr / a.G;
+  const long long dst = (static_cast<long long>(jt.q0) + token) * a.Hq + jt.h * a.G + (rr - token * a.G);
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  uint2 w;
+  w.x = pack_half2<F16>(o.x * inv, o.y * inv);
+  w.y = pack_half2<F16>(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(a.o + dst * 128)[lane] = w;
+  if (lane == 0) a.lse[dst] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace
+
+size_t cache_attn_chunk_workspace(int num_workers) {
+  return num_workers * (sizeof(Joint) + 2 * part_floats<kRowTile>() * sizeof(float));
+}
+
+cudaError_t launch_cache_attn_chunk(const cache::AttnArgs& a, int over, bool f16, int num_workers,
+                                    cudaStream_t stream) {
+  const Share share{over, 0x7fffffff};
+  auto kern = f16 ? cache_attn_chunk_kernel<true> : cache_attn_chunk_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal);
+  if (e != cudaSuccess) return e;
+  kern<<<num_workers, kThreads, kSmemTotal, stream>>>(a, share);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto join = f16 ? cache_attn_join_kernel<true> : cache_attn_join_kernel<false>;
+  join<<<dim3(num_workers, kRowTile / kJoinRows), kJoinRows * 32, 0, stream>>>(a, num_workers);
+  return cudaGetLastError();
+}
+
+}  // namespace vsa

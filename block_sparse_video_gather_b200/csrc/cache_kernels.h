@@ -44,6 +44,11 @@ size_t cache_attn_small_workspace(int num_workers);
 cudaError_t launch_cache_attn_small(const cache::AttnArgs& a, int over, int upto, bool f16, int rows, int num_sms,
                                     cudaStream_t stream);
 
+// cache_attn_chunk.cu: requests of more than `over` rows.
+size_t cache_attn_chunk_workspace(int num_workers);
+cudaError_t launch_cache_attn_chunk(const cache::AttnArgs& a, int over, bool f16, int num_workers,
+                                    cudaStream_t stream);
+
 // merge.cu
 cudaError_t launch_untile_merge(const Geo& g, int B, int H, const uint16_t* ot, const float* lse_t,
                                 const uint16_t* past, const float* lse_past, uint16_t* o, float* lse, bool f16,
