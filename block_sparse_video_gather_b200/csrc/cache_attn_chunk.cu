@@ -51,8 +51,8 @@ constexpr uint32_t kSmemV = kSmemK + kStagesK * kTileBytes;
 constexpr uint32_t kSmemBar = kSmemV + kStagesV * kTileBytes;
 constexpr uint32_t kSmemTotal = kSmemBar + 512 + 1024;  // barriers, segments + 1 KB alignment slack
 constexpr uint64_t kTimeoutNs = 2000000000ull;          // 2 s per wait
-// Register split: launched at 128 per thread; 128 x (72 + 88) + 256 x 176 = 512 x 128.
-constexpr int kRegsMma = 72, kRegsLoad = 88, kRegsRows = 176;
+// Register split: launched at 128 per thread; 128 x (40 + 88) + 256 x 192 = 512 x 128.
+constexpr int kRegsMma = 40, kRegsLoad = 88, kRegsRows = 192;
 static_assert(128 * (kRegsMma + kRegsLoad) + 256 * kRegsRows == kThreads * 128, "register split must match the launch");
 
 using S = Sched<kRowTile, kKeyTile>;
@@ -115,6 +115,44 @@ struct SegReader {
     return seg;
   }
 };
+
+// The eight K = 16 products of a tile, one lane issuing.  Descriptors are put
+// together from their low words inside the block: with 64-bit operands handed
+// in one by one the compiler keeps all of them in registers, spills, and the
+// issue (5200 cycles per unit where the products take 2050) bounds the kernel.
+#define VSA_MMA_SS(OFF, ACC)                                                          \
+  "add.u32 x, %1, " #OFF ";\n\tadd.u32 y, %2, " #OFF ";\n\t"                           \
+  "mov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"                                  \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " #ACC ";\n\t"
+// D[tmem] = A[smem] B[smem], both K-major: 32 bytes of a 128-byte column a step, then the other column.
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred e, yes, no;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.eq.b32 yes, %3, %3;\n\tsetp.ne.b32 no, %3, %3;\n\t" VSA_MMA_SS(0, no) VSA_MMA_SS(2, yes)
+          VSA_MMA_SS(4, yes) VSA_MMA_SS(6, yes) VSA_MMA_SS(1024, yes) VSA_MMA_SS(1026, yes) VSA_MMA_SS(1028, yes)
+              VSA_MMA_SS(1030, yes) "}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc)
+      : "memory");
+}
+#undef VSA_MMA_SS
+#define VSA_MMA_TS(STEP, ACC)                                                         \
+  "add.u32 x, %1, 8 * " #STEP ";\n\tadd.u32 y, %2, 128 * " #STEP ";\n\t"              \
+  "mov.b64 db, {y, %3};\n\t"                                                          \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, " #ACC ";\n\t"
+// D[tmem] (+)= A[tmem] B[smem], B MN-major: 16 rows (2048 bytes) a step.
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t desc_hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, yes, acc;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.eq.b32 yes, %3, %3;\n\tsetp.ne.b32 acc, %5, 0;\n\t" VSA_MMA_TS(0, acc) VSA_MMA_TS(1, yes)
+          VSA_MMA_TS(2, yes) VSA_MMA_TS(3, yes) VSA_MMA_TS(4, yes) VSA_MMA_TS(5, yes) VSA_MMA_TS(6, yes)
+              VSA_MMA_TS(7, yes) "}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+#undef VSA_MMA_TS
 
 // 16 channels of a key, code times scale, as two 16-byte chunks of a tile.
 __device__ __forceinline__ void put_chunk(uint8_t* dst, uint32_t word, uint32_t scale) {
@@ -215,31 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 0) {
       // ------------------------------------------------------------ MMA issuer
-      const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kHalfBytes, 1024);
-      constexpr uint64_t kTileDesc = kTileBytes >> 4;
+      // shared-memory descriptors (128-byte swizzle), low words; the high word is the same for all
+      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint32_t dq0 = static_cast<uint32_t>(dq), desc_hi = static_cast<uint32_t>(dq >> 32);
+      const uint32_t dk0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sK), 16, 1024));
+      const uint32_t dv0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(sV), kHalfBytes, 1024));
+      constexpr uint32_t kTileDesc = kTileBytes >> 4;
       constexpr uint32_t kIdescS = idesc_f16_f32(128, 128, 0, 0), kIdescPV = idesc_f16_f32(128, 128, 0, 1);
       int sk = 0, sv = 0;                // ring places
       uint32_t pk = 0, pv = 0;           // and their parities
       uint32_t pq = 0, pp[2] = {0, 0}, po[2] = {1, 1};
       bool ok = true;
       auto issue_s = [&](int i) {
-        const uint32_t d = tmem + i * 128;
-        const uint64_t qa = dq0 + i * kTileDesc, b = dk0 + sk * kTileDesc;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-          mma_ss_w(d, qa + off, b + off, kIdescS, kk > 0 ? 1u : 0u);
-        }
+        mma8_ss(tmem + i * 128, dq0 + i * kTileDesc, dk0 + sk * kTileDesc, desc_hi, kIdescS);
         mma_commit_w(&bars->s_full[i]);
       };
       auto issue_pv = [&](int i, bool acc) {
-        const uint32_t d = tmem + 256 + i * 128, pa = tmem + i * 128;
-        const uint64_t b = dv0 + sv * kTileDesc;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts_w(d, pa + kk * 8, b + kk * (2048 >> 4), kIdescPV, (acc || kk > 0) ? 1u : 0u);
+        mma8_ts(tmem + 256 + i * 128, tmem + i * 128, dv0 + sv * kTileDesc, desc_hi, kIdescPV, acc);
       };
       auto k_done = [&]() {
         mma_commit_w(&bars->k_empty[sk]);
@@ -318,22 +348,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kw[16], vw[16], ks[4], vs[4];
     int live = 0;  // keys of the record pair that hold a token, from 0; bad pages hold none
     const uint8_t* rec[2];
-    auto place = [&](const Seg& cu, int t) {
+    unsigned page[2];  // pages of the warp's two records of the next tile, asked for one tile before
+    auto ask = [&](const Seg& cu, int t) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = t * 8 + w * 2 + x;  // record of the request
-        rec[x] = nullptr;
-        if (r * kRecTokens < cu.kv) {
-          const unsigned page =
-              __ldg(a.table + static_cast<long long>(cu.r) * a.max_pages + (r >> log_rec));
-          if (page < static_cast<unsigned>(a.num_pages))
-            rec[x] = a.pages + static_cast<unsigned long long>(page) * page_bytes +
-                     ((static_cast<long long>(cu.h) << log_rec) + (r & ((1 << log_rec) - 1))) * kRecBytes;
-          else if (lane == 0)
-            atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
-        }
+        page[x] = r * kRecTokens < cu.kv
+                      ? static_cast<unsigned>(__ldg(a.table + static_cast<long long>(cu.r) * a.max_pages + (r >> log_rec)))
+                      : 0u;
       }
+    };
+    auto place = [&](const Seg& cu, int t) {
       live = cu.kv - (t * kKeyTile + w * 32);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = t * 8 + w * 2 + x;
+        rec[x] = nullptr;
+        if (page[x] < static_cast<unsigned>(a.num_pages))
+          rec[x] = a.pages + static_cast<unsigned long long>(page[x]) * page_bytes +
+                   ((static_cast<long long>(cu.h) << log_rec) + (r & ((1 << log_rec) - 1))) * kRecBytes;
+        else if (lane == 0)
+          atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+      }
     };
     auto load_k = [&]() {
 #pragma unroll
@@ -386,8 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     SegReader segs;
     Seg cur = segs.next(bars, a.status);
     int t = 0;
-    if (cur.n > 0) {
+    auto first_of = [&]() {  // the first tile of a segment: its pages, and the next tile's
+      ask(cur, cur.k0);
       place(cur, cur.k0);
+      if (cur.n > 1) ask(cur, cur.k0 + 1);
+    };
+    if (cur.n > 0) {
+      first_of();
       load_k();
     }
     while (cur.n > 0 && ok) {
@@ -402,11 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++t == cur.n) {
         t = 0;
         cur = segs.next(bars, a.status);
-      }
-      if (cur.n > 0) {
+        if (cur.n > 0) first_of();
+      } else {
         place(cur, cur.k0 + t);
-        load_k();
+        if (t + 1 < cur.n) ask(cur, cur.k0 + t + 1);
       }
+      if (cur.n > 0) load_k();
       if (!(ok = warp_wait(&bars->v_empty[sv], pv, bars, a.status))) break;
       store(sV + sv * kTileBytes, vw, vs);
       mbar_arrive(&bars->v_full[sv]);
@@ -477,17 +519,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&bars->q_full);
       const float sl2 = a.scale_log2 * inv;
 
+      // pages of a tile's eight records, one a lane, asked for one tile before
+      auto page_at = [&](int t) -> unsigned {
+        const int rec = (cur.k0 + t) * (kKeyTile / kRecTokens) + lane;
+        if (lane >= 8 || rec * kRecTokens >= cur.kv) return 0u;
+        return static_cast<unsigned>(__ldg(a.table + static_cast<long long>(cur.r) * a.max_pages + (rec >> log_rec)));
+      };
+      unsigned page = page_at(0);
       float m_used = -INFINITY, l = 0.0f;
       for (int t = 0; t < n && active; ++t) {
         const int key0 = (cur.k0 + t) * kKeyTile;
-        // pages of the tile's eight records, one a lane
-        bool bad = false;
-        if (lane < 8 && key0 + lane * kRecTokens < cur.kv) {
-          const unsigned page = __ldg(a.table + static_cast<long long>(cur.r) * a.max_pages +
-                                      (((key0 >> 4) + lane) >> log_rec));
-          bad = page >= static_cast<unsigned>(a.num_pages);
-        }
-        const unsigned bad_recs = __ballot_sync(0xffffffffu, bad);
+        const unsigned bad_recs = __ballot_sync(0xffffffffu, page >= static_cast<unsigned>(a.num_pages));
+        if (t + 1 < n) page = page_at(t + 1);
         if (!(ok = warp_wait(&bars->s_full[wg], ps, bars, a.status))) break;
         ps ^= 1;
         tc_fence_after();
