@@ -536,56 +536,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float alpha = 1.0f;
         bool rescale = false;
-        {
-          uint32_t sv[128];
-          tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
-          tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-          tmem_wait_ld();
-          const int see = lim - key0;  // columns this row sees
-          if (see < kKeyTile || bad_recs) {
+        uint32_t sv[128];
+        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
+        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
+        tmem_wait_ld();
+        const int see = lim - key0;  // columns this row sees
+        if (see < kKeyTile || bad_recs) {
 #pragma unroll
-            for (int x = 0; x < 128; ++x)
-              if (x >= see || (bad_recs >> (x >> 4) & 1)) sv[x] = 0xff800000u;
-          }
-          float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < 128; x += 8) {
-            a0 = max3f(a0, __uint_as_float(sv[x + 0]), __uint_as_float(sv[x + 1]));
-            a1 = max3f(a1, __uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3]));
-            a2 = max3f(a2, __uint_as_float(sv[x + 4]), __uint_as_float(sv[x + 5]));
-            a3 = max3f(a3, __uint_as_float(sv[x + 6]), __uint_as_float(sv[x + 7]));
-          }
-          const float mt = max3f(a0, a1, fmaxf(a2, a3)) * sl2;
-          const bool grow = mt > m_used + 8.0f;
-          rescale = grow && t > 0 && m_used != -INFINITY;
-          alpha = rescale ? ex2_approx(m_used - mt) : 1.0f;
-          if (grow) m_used = mt;
+          for (int x = 0; x < 128; ++x)
+            if (x >= see || (bad_recs >> (x >> 4) & 1)) sv[x] = 0xff800000u;
+        }
+        // The numerators are taken against the maximum so far while the tile's own is found; only where a row's
+        // exceeds it by more than 8 (always in a segment's first tile) are they taken again.
+        float part;
+        while (true) {
           const float msub = (m_used == -INFINITY) ? 0.0f : m_used;
           const uint64_t c2 = f2pack(sl2, sl2), nm2 = f2pack(-msub, -msub);
-          uint64_t acc[4] = {0, 0, 0, 0};
+          uint64_t acc[2] = {0, 0};
+          float a0 = -INFINITY, a1 = -INFINITY;
+          const bool first = t == 0 && m_used == -INFINITY;
+          if (__all_sync(0xffffffffu, first)) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t pk[32];
+            for (int x = 0; x < 128; x += 4) {
+              a0 = max3f(a0, __uint_as_float(sv[x + 0]), __uint_as_float(sv[x + 1]));
+              a1 = max3f(a1, __uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3]));
+            }
+            const float mt = fmaxf(a0, a1) * sl2;
+            if (mt > -INFINITY) m_used = mt;
+            if (__any_sync(0xffffffffu, mt > -INFINITY)) continue;
+          }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const uint64_t x = fma2(u2pack(sv[64 * hf + 2 * j], sv[64 * hf + 2 * j + 1]), c2, nm2);
+          for (int hf = 0; hf < 4; ++hf) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t u = sv[32 * hf + 2 * j], v = sv[32 * hf + 2 * j + 1];
+              if (j & 1) a1 = max3f(a1, __uint_as_float(u), __uint_as_float(v));
+              else a0 = max3f(a0, __uint_as_float(u), __uint_as_float(v));
+              const uint64_t x = fma2(u2pack(u, v), c2, nm2);
               float xa, xb;
               f2unpack(x, xa, xb);
               const float p0 = ex2_approx(xa), p1 = ex2_approx(xb);
               pk[j] = pack_f16x2(p0, p1);
-              acc[j & 3] = add2(acc[j & 3], f2pack(p0, p1));
+              acc[j & 1] = add2(acc[j & 1], f2pack(p0, p1));
             }
-            tmem_st32(tS + 32 * hf, pk);
+            tmem_st16(tS + 16 * hf, pk);
           }
-          float s0, s1, s2, s3, s4, s5, s6, s7;
+          float s0, s1, s2, s3;
           f2unpack(acc[0], s0, s1);
           f2unpack(acc[1], s2, s3);
-          f2unpack(acc[2], s4, s5);
-          f2unpack(acc[3], s6, s7);
-          l = l * alpha + (((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7)));
+          part = (s0 + s1) + (s2 + s3);
+          const float mt = fmaxf(a0, a1) * sl2;
+          const bool grow = mt > m_used + 8.0f;
+          if (!__any_sync(0xffffffffu, grow)) break;
+          if (grow) {
+            rescale = t > 0 && m_used != -INFINITY;
+            alpha = rescale ? ex2_approx(m_used - mt) : 1.0f;
+            m_used = mt;
+          }
         }
+        l = l * alpha + part;
         // Rescale this row of O when its maximum moved.  PV(t-1) is complete: the s_full commit just waited on
         // follows it in issue order.
         if (__any_sync(0xffffffffu, rescale)) {
