@@ -17,6 +17,7 @@ the selection, and untile_gate sums the two branches under the caller's gate.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -479,18 +480,47 @@ def sparse_attn_bwd(plan: Plan, q, k, v, o, lse, do, q2k_idx, q2k_num, dq=None, 
     return dq, dk, dv
 
 
+_torch_module = None
+
+
+def _device_and_stream(t, what):
+    """(ordinal, raw stream) of a CUDA tensor's device, which must be the current one: the library launches there.
+    The calls on the cache are short and made once a token and layer, so their binding looks things up once."""
+    global _torch_module
+    if _torch_module is None:
+        _torch_module = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    dev = t.get_device()
+    current = _torch_module.cuda.current_device()
+    if dev != current:
+        raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{current}")
+    return dev, _torch_module._C._cuda_getCurrentRawStream(dev)
+
+
+def _at(t, dtype, dev, what):
+    """The address of a contiguous tensor of a type on a device."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the others on cuda:{dev}")
+    raise ValueError(f"{what} must be contiguous")
+
+
 def _rows(t, what):
     """A [T, heads, 128] tensor whose tokens may be strided (a slice of a fused projection):
     (pointer, elements from token to token)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
     if t.dim() != 3 or t.shape[2] != 128:
         raise ValueError(f"{what} must be [tokens, heads, 128], got {tuple(t.shape)}")
     T, H, D = t.shape
     st = t.stride()
     if st[2] != 1 or (H > 1 and st[1] != D):
         raise ValueError(f"{what}: heads and channels must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (st[0] if T > 1 else max(st[0], H * D) & ~7)
+    return t.data_ptr(), (st[0] if T > 1 else max(st[0], H * D) & ~7)
 
 
 def _pages_shape(pages):
@@ -515,11 +545,12 @@ def cache_tables(kv_len, new_len, page_tokens: int, free_pages, free_start, bloc
     [R, max_pages] and the new tokens' slots (all of `slots`; -1 past the last), and returns (kv_len_out [R],
     cu [R + 1], free_next [1]).  See vsa_cache_tables; kv_len_out and free_next must be other tensors than kv_len
     and free_start."""
-    torch = _torch()
-    i32 = torch.int32
     R = kv_len.shape[0]
     if kv_len.shape != (R,) or new_len.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("kv_len and new_len must be [R], block_table [R, max_pages]")
+    dev, stream = _device_and_stream(kv_len, "kv_len")
+    torch = _torch_module
+    i32 = torch.int32
     if kv_len_out is None:
         kv_len_out = torch.empty_like(kv_len)
     if cu_out is None:
@@ -529,25 +560,27 @@ def cache_tables(kv_len, new_len, page_tokens: int, free_pages, free_start, bloc
     if kv_len_out.numel() != R or cu_out.numel() != R + 1 or free_next_out.numel() < 1 or free_start.numel() < 1:
         raise ValueError("kv_len_out must hold R, cu_out R + 1, free_start and free_next_out 1 entries")
     _check(lib().vsa_cache_tables(
-        _ptr(kv_len, i32, "kv_len"), _ptr(new_len, i32, "new_len"), R, page_tokens,
-        _ptr(free_pages, i32, "free_pages"), free_pages.numel(), _ptr(free_start, i32, "free_start"),
-        _ptr(block_table, i32, "block_table"), block_table.shape[1], _ptr(kv_len_out, i32, "kv_len_out"),
-        _ptr(cu_out, i32, "cu_out"), _ptr(slots, i32, "slots"), slots.numel(),
-        _ptr(free_next_out, i32, "free_next_out"), _stream()), "vsa_cache_tables")
+        _at(kv_len, i32, dev, "kv_len"), _at(new_len, i32, dev, "new_len"), R, page_tokens,
+        _at(free_pages, i32, dev, "free_pages"), free_pages.numel(), _at(free_start, i32, dev, "free_start"),
+        _at(block_table, i32, dev, "block_table"), block_table.shape[1], _at(kv_len_out, i32, dev, "kv_len_out"),
+        _at(cu_out, i32, dev, "cu_out"), _at(slots, i32, dev, "slots"), slots.numel(),
+        _at(free_next_out, i32, dev, "free_next_out"), stream), "vsa_cache_tables")
     return kv_len_out, cu_out, free_next_out
 
 
 def cache_release(drop, page_tokens: int, kv_len, block_table, free_pages, free_start):
     """Gives the pages of the requests with drop[r] != 0 back to the stack and sets their kv_len to 0, in place."""
-    i32 = _torch().int32
+    dev, stream = _device_and_stream(kv_len, "kv_len")
+    i32 = _torch_module.int32
     R = kv_len.shape[0]
     if drop.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("drop and kv_len must be [R], block_table [R, max_pages]")
-    d = drop.view(_torch().uint8) if drop.dtype == _torch().bool else drop
+    u8 = _torch_module.uint8
+    d = drop.view(u8) if drop.dtype == _torch_module.bool else drop
     _check(lib().vsa_cache_release(
-        _ptr(d, _torch().uint8, "drop"), R, page_tokens, _ptr(kv_len, i32, "kv_len"),
-        _ptr(block_table, i32, "block_table"), block_table.shape[1], _ptr(free_pages, i32, "free_pages"),
-        free_pages.numel(), _ptr(free_start, i32, "free_start"), _stream()), "vsa_cache_release")
+        _at(d, u8, dev, "drop"), R, page_tokens, _at(kv_len, i32, dev, "kv_len"),
+        _at(block_table, i32, dev, "block_table"), block_table.shape[1], _at(free_pages, i32, dev, "free_pages"),
+        free_pages.numel(), _at(free_start, i32, dev, "free_start"), stream), "vsa_cache_release")
 
 
 def cache_append(k, v, slots, pages):
@@ -562,10 +595,13 @@ def cache_append(k, v, slots, pages):
         raise ValueError(f"slots must be [{T}], got {tuple(slots.shape)}")
     if T == 0:
         return
+    dev, stream = _device_and_stream(pages, "pages")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be on cuda:{dev}")
     kp, ks = _rows(k, "k")
     vp, vs = _rows(v, "v")
-    _check(lib().vsa_cache_append_nvfp4(code, kp, vp, ks, vs, _ptr(slots, _torch().int32, "slots"), T, Hkv, D,
-                                        _ptr(pages, _torch().uint8, "pages"), n, page_tokens, _stream()),
+    _check(lib().vsa_cache_append_nvfp4(code, kp, vp, ks, vs, _at(slots, _torch_module.int32, dev, "slots"), T, Hkv, D,
+                                        _at(pages, _torch_module.uint8, dev, "pages"), n, page_tokens, stream),
            "vsa_cache_append_nvfp4")
 
 
@@ -586,17 +622,23 @@ def cache_read(slots, pages, dtype=None, k_out=None, v_out=None):
         raise ValueError(f"k_out and v_out must be [{T}, {Hkv}, 128]")
     if T == 0:
         return k_out, v_out
-    _check(lib().vsa_cache_read_nvfp4(_dtype_code(k_out, "k_out"), _ptr(slots, torch.int32, "slots"), T, Hkv, 128,
-                                      _ptr(pages, torch.uint8, "pages"), n, page_tokens, _ptr(k_out, dtype, "k_out"),
-                                      _ptr(v_out, dtype, "v_out"), _stream()), "vsa_cache_read_nvfp4")
+    dev, stream = _device_and_stream(pages, "pages")
+    _check(lib().vsa_cache_read_nvfp4(_dtype_code(k_out, "k_out"), _at(slots, torch.int32, dev, "slots"), T, Hkv, 128,
+                                      _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(k_out, dtype, dev, "k_out"),
+                                      _at(v_out, dtype, dev, "v_out"), stream), "vsa_cache_read_nvfp4")
     return k_out, v_out
+
+
+@functools.lru_cache(maxsize=None)
+def _attn_workspace_bytes(Hq: int, Hkv: int, max_q: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().vsa_cache_attn_workspace(Hq, Hkv, max_q, ctypes.byref(n)), "vsa_cache_attn_workspace")
+    return n.value
 
 
 def cache_workspace(max_q: int, Hq: int, Hkv: int, device="cuda"):
     """The zeroed workspace of cache_attn calls with at most max_q new tokens a request."""
-    n = ctypes.c_size_t(0)
-    _check(lib().vsa_cache_attn_workspace(Hq, Hkv, max_q, ctypes.byref(n)), "vsa_cache_attn_workspace")
-    return _torch().zeros(n.value, dtype=_torch().uint8, device=device)
+    return _torch().zeros(_attn_workspace_bytes(Hq, Hkv, max_q), dtype=_torch().uint8, device=device)
 
 
 def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal: bool = True, o_out=None,
@@ -604,7 +646,8 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
     """Attention of q [T, Hq, 128] (tokens may be strided) over each request's cached tokens -> (o [T, Hq, 128],
     lse [T, Hq]).  Request r's queries are rows cu[r] .. cu[r+1]; causal: they are the cache's last tokens.
     workspace: cache_workspace of at least this max_q and these heads; left ready for the next call."""
-    torch = _torch()
+    dev, stream = _device_and_stream(q, "q")
+    torch = _torch_module
     n, Hkv, page_tokens = _pages_shape(pages)
     code = _dtype_code(q, "q")
     qp, qs = _rows(q, "q")
@@ -612,10 +655,9 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
     R = kv_len.shape[0]
     if cu.shape != (R + 1,) or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("kv_len must be [R], cu [R + 1], block_table [R, max_pages]")
-    need = ctypes.c_size_t(0)
-    _check(lib().vsa_cache_attn_workspace(Hq, Hkv, max_q, ctypes.byref(need)), "vsa_cache_attn_workspace")
-    if workspace.numel() * workspace.element_size() < need.value:
-        raise ValueError(f"workspace needs {need.value} bytes (cache_workspace)")
+    need = _attn_workspace_bytes(Hq, Hkv, max_q)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace needs {need} bytes (cache_workspace)")
     if o_out is None:
         o_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
     if lse_out is None:
@@ -626,10 +668,10 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
         return o_out, lse_out
     i32 = torch.int32
     _check(lib().vsa_cache_attn_nvfp4(
-        code, qp, qs, _ptr(cu, i32, "cu"), _ptr(kv_len, i32, "kv_len"), R, T, max_q, Hq, Hkv, D,
-        _ptr(pages, torch.uint8, "pages"), n, page_tokens, _ptr(block_table, i32, "block_table"),
-        block_table.shape[1], int(causal), _ptr(o_out, q.dtype, "o"), _ptr(lse_out, torch.float32, "lse"),
-        _ptr(workspace, workspace.dtype, "workspace"), _stream()), "vsa_cache_attn_nvfp4")
+        code, qp, qs, _at(cu, i32, dev, "cu"), _at(kv_len, i32, dev, "kv_len"), R, T, max_q, Hq, Hkv, D,
+        _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(block_table, i32, dev, "block_table"),
+        block_table.shape[1], int(causal), _at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
+        _at(workspace, workspace.dtype, dev, "workspace"), stream), "vsa_cache_attn_nvfp4")
     return o_out, lse_out
 
 
@@ -637,7 +679,8 @@ def untile_merge(plan: Plan, ot, lse, o_past, lse_past, out=None, lse_out=None):
     """o [B,S,H,D] and lse [B,S,H] of the union of two key sets: the fine stage's (ot [B,H,Sp,D], lse [B,H,Sp],
     tiled) and another attention's (o_past [B,S,H,D], lse_past [B,S,H], untiled).  out and lse_out may be o_past
     and lse_past."""
-    torch = _torch()
+    dev, stream = _device_and_stream(ot, "o_tiled")
+    torch = _torch_module
     B, H, Sp, D = ot.shape
     code = _dtype_code(ot, "o_tiled")
     if Sp != plan.Sp:
@@ -651,9 +694,9 @@ def untile_merge(plan: Plan, ot, lse, o_past, lse_past, out=None, lse_out=None):
     if out.shape != o_past.shape or lse_out.shape != lse_past.shape:
         raise ValueError("out and lse_out must have the shapes of o_past and lse_past")
     f32 = torch.float32
-    _check(lib().vsa_untile_merge(plan.handle, code, _ptr(ot, ot.dtype, "o_tiled"), _ptr(lse, f32, "lse"),
-                                  _ptr(o_past, ot.dtype, "o_past"), _ptr(lse_past, f32, "lse_past"), B, H, D,
-                                  _ptr(out, ot.dtype, "o"), _ptr(lse_out, f32, "lse_out"), _stream()),
+    _check(lib().vsa_untile_merge(plan.handle, code, _at(ot, ot.dtype, dev, "o_tiled"), _at(lse, f32, dev, "lse"),
+                                  _at(o_past, ot.dtype, dev, "o_past"), _at(lse_past, f32, dev, "lse_past"), B, H, D,
+                                  _at(out, ot.dtype, dev, "o"), _at(lse_out, f32, dev, "lse_out"), stream),
            "vsa_untile_merge")
     return out, lse_out
 

@@ -43,6 +43,9 @@ using namespace cache;
 constexpr int kThreads = 512;
 constexpr int kRowTile = 256, kKeyTile = 128;
 constexpr int kStagesK = 3, kStagesV = 2, kSegs = 4;
+// An item's rows of Q, first product and output take a CTA some 6 to 9 us, a unit 2.4 us (4 x 1023 on 5000: 157 us with
+// 4, 162 with 3, 170 with 2, 196 with 0; one long item does not care).
+constexpr int kItemCost = 4;
 constexpr uint32_t kHalfBytes = 128 * 128;       // 128 rows x 64 fp16 (one 128-B swizzle column)
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // 128 rows x 128 fp16
 constexpr uint32_t kSmemQ = 0;
@@ -55,7 +58,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;          // 2 s per wait
 constexpr int kRegsMma = 40, kRegsLoad = 88, kRegsRows = 192;
 static_assert(128 * (kRegsMma + kRegsLoad) + 256 * kRegsRows == kThreads * 128, "register split must match the launch");
 
-using S = Sched<kRowTile, kKeyTile>;
+using S = Sched<kRowTile, kKeyTile, kItemCost>;
 
 // Units [k0, k0 + n) of an item; n = 0: the end.
 struct Seg {
@@ -229,26 +232,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       int at = 0;
       uint32_t parity = 1;
       int left = static_cast<int>(ce - cs);
-      while (true) {
-        const int n = min(left, cur.nu - cur.k);
-        if (!warp_wait(&bars->seg_empty[at], parity, bars, a.status)) break;
-        if (lane == 0) {
-          Seg g;
-          g.r = cur.r, g.h = cur.h, g.j = cur.j;
-          g.k0 = cur.k, g.n = n;
-          g.whole = n == cur.nu;
-          g.q0 = cur.req.q0, g.tokens = cur.req.n, g.kv = cur.req.kv;
-          g.last = cur.k == 0 && n < cur.nu ? cut.worker_of(cur.item0 + cur.nu - 1) : -1;
-          bars->seg[at] = g;
-          mbar_arrive(&bars->seg_full[at]);
+      bool end = false;
+      while (!end) {
+        const int places = min(left, cur.nu - cur.k);
+        const int units = cur.nu - kItemCost, k0 = max(0, cur.k - kItemCost), k1 = cur.k + places - kItemCost;
+        end = left == 0;
+        if (end || k1 > k0) {
+          if (!warp_wait(&bars->seg_empty[at], parity, bars, a.status)) break;
+          if (lane == 0) {
+            Seg g;
+            g.r = cur.r, g.h = cur.h, g.j = cur.j;
+            g.k0 = k0, g.n = end ? 0 : k1 - k0;
+            g.whole = k0 == 0 && k1 == units;
+            g.q0 = cur.req.q0, g.tokens = cur.req.n, g.kv = cur.req.kv;
+            g.last = k0 == 0 && k1 < units ? cut.worker_of(cur.item0 + cur.nu - 1) : -1;
+            bars->seg[at] = g;
+            mbar_arrive(&bars->seg_full[at]);
+          }
+          __syncwarp();
+          if (++at == kSegs) {
+            at = 0;
+            parity ^= 1;
+          }
         }
-        __syncwarp();
-        if (n == 0) break;  // the end has been handed on
-        if (++at == kSegs) {
-          at = 0;
-          parity ^= 1;
-        }
-        left -= n;
+        left -= places;
         if (left > 0) cur.next_item(a, share);
       }
     } else if (warp == 0) {
@@ -484,36 +491,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long dst = (static_cast<long long>(cur.q0) + token) * a.Hq + head;
       const int lim = visible(a, Request{cur.q0, cur.tokens, cur.kv}, token);
 
-      // ---- Q row -> fp16, swizzled; the row's scale goes into the softmax
+      // ---- Q rows -> fp16, swizzled; a row's scale goes into its thread's softmax.  The warp loads two rows a step,
+      // 16 lanes a row, so that every access takes whole rows; each lane knows where its own row is.
       float inv = 1.0f;
+      const long long q_at =
+          real ? (static_cast<long long>(cur.q0) + token) * a.q_stride + static_cast<long long>(head) * 128 : -1;
       if (!(ok = warp_wait(&bars->q_empty, pq, bars, a.status))) break;
       pq ^= 1;
+      uint8_t* q_rows = sQ + wg * kTileBytes + quarter * 32 * 128;  // the warp's 32 rows, two columns
+      const int sub = lane & 15, upper = lane >> 4;
       if (active) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(a.q + (static_cast<long long>(cur.q0) + token) * a.q_stride + head * 128);
-        uint32_t qw[64];
+        uint4 qv[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (real) v = __ldg(src + x);
-          qw[4 * x] = v.x, qw[4 * x + 1] = v.y, qw[4 * x + 2] = v.z, qw[4 * x + 3] = v.w;
+        for (int i = 0; i < 16; ++i) {
+          const long long at = __shfl_sync(0xffffffffu, q_at, 2 * i + upper);
+          qv[i] = make_uint4(0, 0, 0, 0);
+          if (at >= 0) qv[i] = __ldg(reinterpret_cast<const uint4*>(a.q + at) + sub);
         }
-        if (!F16) {
-          float amax = 0.0f;
 #pragma unroll
-          for (int x = 0; x < 64; ++x) amax = max3f(amax, fabsf(bf16_lo(qw[x])), fabsf(bf16_hi(qw[x])));
-          const int e = __float_as_uint(amax) >> 23;
-          const int upb = amax == 0.0f || e == 255 ? 0 : min(141 - e, 100);  // 2^upb * amax in [2^14, 2^15)
-          const float f = __uint_as_float((upb + 127) << 23);
-          inv = __uint_as_float((127 - upb) << 23);
+        for (int i = 0; i < 16; ++i) {
+          const int row2 = 2 * i + upper;
+          const uint4 v = qv[i];
+          uint32_t qw[4] = {v.x, v.y, v.z, v.w};
+          if (!F16) {
+            float amax = 0.0f;
 #pragma unroll
-          for (int x = 0; x < 64; ++x) qw[x] = pack_f16x2(bf16_lo(qw[x]) * f, bf16_hi(qw[x]) * f);
+            for (int x = 0; x < 4; ++x) amax = max3f(amax, fabsf(bf16_lo(qw[x])), fabsf(bf16_hi(qw[x])));
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            const int e = __float_as_uint(amax) >> 23;
+            const int upb = amax == 0.0f || e == 255 ? 0 : min(141 - e, 100);  // 2^upb * amax in [2^14, 2^15)
+            const float f = __uint_as_float((upb + 127) << 23);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) qw[x] = pack_f16x2(bf16_lo(qw[x]) * f, bf16_hi(qw[x]) * f);
+            const float back = __shfl_sync(0xffffffffu, __uint_as_float((127 - upb) << 23), (lane & 1) * 16);
+            if (lane >> 1 == i) inv = back;
+          }
+          *reinterpret_cast<uint4*>(q_rows + (sub >> 3) * kHalfBytes + row2 * 128 + (((sub & 7) ^ (row2 & 7)) << 4)) =
+              make_uint4(qw[0], qw[1], qw[2], qw[3]);
         }
-        uint8_t* q_row = sQ + wg * kTileBytes + r * 128;
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          *reinterpret_cast<uint4*>(q_row + (x >> 3) * kHalfBytes + (((x & 7) ^ (r & 7)) << 4)) =
-              make_uint4(qw[4 * x], qw[4 * x + 1], qw[4 * x + 2], qw[4 * x + 3]);
         fence_proxy_async_smem();
       }
       mbar_arrive(&bars->q_full);
@@ -621,25 +637,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         po ^= 1;
         tc_fence_after();
         if (cur.whole) {
+          // through the warp's rows of Q, which no product reads any more, so that whole rows are stored
           const float scale = l != 0.0f ? 1.0f / l : 0.0f;
-          uint4* orow = reinterpret_cast<uint4*>(a.o + dst * 128);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t ov[32];
             tmem_ld32(tO + x * 32, ov);
             tmem_wait_ld();
-            uint4 o4[4];
-            uint32_t* wp = reinterpret_cast<uint32_t*>(o4);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              wp[j] = pack_half2<F16>(__uint_as_float(ov[2 * j]) * scale, __uint_as_float(ov[2 * j + 1]) * scale);
-            if (real) {
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) orow[x * 4 + j] = o4[j];
+              for (int y = 0; y < 4; ++y)
+                w[y] = pack_half2<F16>(__uint_as_float(ov[8 * j + 2 * y]) * scale, __uint_as_float(ov[8 * j + 2 * y + 1]) * scale);
+              const int chunk = 4 * x + j;
+              *reinterpret_cast<uint4*>(q_rows + (chunk >> 3) * kHalfBytes + lane * 128 + (((chunk & 7) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+          __syncwarp();
+          const long long o_at = real ? dst : -1;
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int row2 = 2 * i + upper;
+            const long long at = __shfl_sync(0xffffffffu, o_at, row2);
+            const uint4 v = *reinterpret_cast<const uint4*>(q_rows + (sub >> 3) * kHalfBytes + row2 * 128 +
+                                                            (((sub & 7) ^ (row2 & 7)) << 4));
+            if (at >= 0) reinterpret_cast<uint4*>(a.o + at * 128)[sub] = v;
+          }
           if (real) a.lse[dst] = l != 0.0f ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          __syncwarp();  // read before the next item's Q takes the rows
         } else {
+          // four channels of 256 rows after another: the threads of a warp store 512 bytes in a row
           float* part = parts_of(a.ws, N) + (static_cast<size_t>(cta) * 2 + (cur.k0 > 0 ? 0 : 1)) * part_floats<kRowTile>();
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -647,9 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + x * 32, ov);
             tmem_wait_ld();
             if (real) {
-              uint4* out = reinterpret_cast<uint4*>(part + row * 128 + x * 32);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) out[j] = make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
+              for (int j = 0; j < 8; ++j)
+                reinterpret_cast<uint4*>(part)[(x * 8 + j) * kRowTile + row] =
+                    make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
             }
           }
           if (real) {
@@ -673,39 +703,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the rows of the items that more than one CTA worked on: a warp per row.
-constexpr int kJoinRows = 8;
+// Joins the rows of the items that more than one CTA worked on.  A CTA takes 32
+// rows, a lane a row, a warp 16 of its channels: reads of 512 bytes in a row.
+constexpr int kJoinRows = 32, kJoinWarps = 8;
 template <bool F16>
-__global__ void __launch_bounds__(kJoinRows * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ AttnArgs a, int workers) {
-  const int first = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int first = blockIdx.x, warp = threadIdx.x >> 5;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x & 31);
   const Joint jt = static_cast<const Joint*>(a.ws)[first];
   if (jt.last < 0 || row >= jt.rows) return;
   constexpr size_t kPart = part_floats<kRowTile>();
   const float* parts = parts_of(a.ws, workers);
   float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+  float o[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) o[x] = 0.0f;
+#pragma unroll 2
   for (int w = first; w <= jt.last; ++w) {
     const float* f = parts + (static_cast<size_t>(w) * 2 + (w == first ? 1 : 0)) * kPart;
-    const float4 po = reinterpret_cast<const float4*>(f + row * 128)[lane];
+    float4 p[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) p[x] = reinterpret_cast<const float4*>(f)[(warp * 4 + x) * kRowTile + row];
     const float pm = f[kRowTile * 128 + row], pl = f[kRowTile * 129 + row];
     const float mn = fmaxf(m, pm);
     // without a maximum a part has nothing but zeros, or the NaN of its scores
     const float w0 = m == -INFINITY ? 1.0f : ex2_approx(m - mn), w1 = pm == -INFINITY ? 1.0f : ex2_approx(pm - mn);
-    o = make_float4(w0 * o.x + w1 * po.x, w0 * o.y + w1 * po.y, w0 * o.z + w1 * po.z, w0 * o.w + w1 * po.w);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      o[4 * x] = w0 * o[4 * x] + w1 * p[x].x;
+      o[4 * x + 1] = w0 * o[4 * x + 1] + w1 * p[x].y;
+      o[4 * x + 2] = w0 * o[4 * x + 2] + w1 * p[x].z;
+      o[4 * x + 3] = w0 * o[4 * x + 3] + w1 * p[x].w;
+    }
     l = w0 * l + w1 * pl;
     m = mn;
   }
   const int rr = jt.j * kRowTile + row, token = rr / a.G;
   const long long dst = (static_cast<long long>(jt.q0) + token) * a.Hq + jt.h * a.G + (rr - token * a.G);
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  uint2 w;
-  w.x = pack_half2<F16>(o.x * inv, o.y * inv);
-  w.y = pack_half2<F16>(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(a.o + dst * 128)[lane] = w;
-  if (lane == 0) a.lse[dst] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+  uint32_t w[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) w[x] = pack_half2<F16>(o[2 * x] * inv, o[2 * x + 1] * inv);
+  uint4* out = reinterpret_cast<uint4*>(a.o + dst * 128 + warp * 16);
+  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (warp == 0) a.lse[dst] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
@@ -718,13 +761,14 @@ cudaError_t launch_cache_attn_chunk(const cache::AttnArgs& a, int over, bool f16
                                     cudaStream_t stream) {
   const Share share{over, 0x7fffffff};
   auto kern = f16 ? cache_attn_chunk_kernel<true> : cache_attn_chunk_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal);
+  static SmemAllowed allowed[2];  // fp16, bf16
+  cudaError_t e = allowed[f16 ? 0 : 1].ensure(reinterpret_cast<const void*>(kern), kSmemTotal);
   if (e != cudaSuccess) return e;
   kern<<<num_workers, kThreads, kSmemTotal, stream>>>(a, share);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   auto join = f16 ? cache_attn_join_kernel<true> : cache_attn_join_kernel<false>;
-  join<<<dim3(num_workers, kRowTile / kJoinRows), kJoinRows * 32, 0, stream>>>(a, num_workers);
+  join<<<dim3(num_workers, kRowTile / kJoinRows), kJoinWarps * 32, 0, stream>>>(a, num_workers);
   return cudaGetLastError();
 }
 

@@ -130,7 +130,7 @@ template <int NT, bool F16, int W, int STAGES>
 __global__ void __launch_bounds__(W * 32, 1)
     cache_attn_small_kernel(const __grid_constant__ AttnArgs a, const Share share) {
   constexpr int RT = 8 * NT;
-  using S = Sched<RT, kUnit>;
+  using S = Sched<RT, kUnit, 0>;
   using Sm = Smem<NT, W, STAGES>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
@@ -592,7 +592,8 @@ cudaError_t launch_small(const AttnArgs& a, const Share& share, bool f16, int nu
   auto kern = f16 ? cache_attn_small_kernel<NT, true, W, STAGES> : cache_attn_small_kernel<NT, false, W, STAGES>;
   constexpr int smem = static_cast<int>(sizeof(Smem<NT, W, STAGES>));
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemAllowed allowed[2];  // fp16, bf16
+  cudaError_t e = allowed[f16 ? 0 : 1].ensure(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   kern<<<num_sms < kMaxWorkers ? num_sms : kMaxWorkers, W * 32, smem, stream>>>(a, share);
   return cudaGetLastError();

@@ -2,6 +2,7 @@
 // and of the merge with the fine stage (not public ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -9,6 +10,25 @@
 #include "common.cuh"
 
 namespace vsa {
+
+// A kernel's shared-memory limit, raised on its first launch on each device (the
+// attribute call costs as much as a short launch).
+class SmemAllowed {
+ public:
+  cudaError_t ensure(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<unsigned long long> done_{0};
+};
 
 // cache.cu
 struct CacheTablesArgs {

@@ -42,8 +42,12 @@ __device__ __forceinline__ long long div_small(long long a, long long b) {
   return a / b;
 }
 
-template <int RT, int KT>
+// COST: places of the line that an item takes before its first unit, for the
+// time a worker spends on an item whatever its length (its rows of Q, the first
+// product, the output); they hold no work.
+template <int RT, int KT, int COST>
 struct Sched {
+  static constexpr int kCost = COST;
   static __device__ __forceinline__ int tiles(const AttnArgs& a, const Request& q) { return (q.n * a.G + RT - 1) / RT; }
   // Cached tokens that tile j's last row sees.
   static __device__ __forceinline__ int keys(const AttnArgs& a, const Request& q, int j) {
@@ -51,11 +55,11 @@ struct Sched {
     return visible(a, q, last / a.G);
   }
   static __device__ __forceinline__ int units(const AttnArgs& a, const Request& q, int j) {
-    return max(1, (keys(a, q, j) + KT - 1) / KT);
+    return COST + max(1, (keys(a, q, j) + KT - 1) / KT);
   }
-  // Units of tiles 0 .. j-1.
+  // Places of tiles 0 .. j-1.
   static __device__ __forceinline__ long long units_before(const AttnArgs& a, const Request& q, int j) {
-    if (!a.causal) return static_cast<long long>(max(1, (q.kv + KT - 1) / KT)) * j;
+    if (!a.causal) return static_cast<long long>(COST + max(1, (q.kv + KT - 1) / KT)) * j;
     if (j <= 1) return j == 0 ? 0 : units(a, q, 0);
     // whole tiles i: the last row's token is floor((RT (i + 1) - 1) / G), it sees kv - n + 1 more than that many
     // tokens, which is floor((RT (i + 1) - 1 + G (kv - n + KT)) / (G KT)) units, or 1 where that is less
@@ -63,7 +67,7 @@ struct Sched {
     const long long G = a.G, c = q.kv - q.n;
     const long long short_of = 1 - G * c;  // RT (i + 1) must reach this for the first whole unit
     const long long i0 = min(static_cast<long long>(n), short_of <= RT ? 0 : (short_of + RT - 1) / RT - 1);
-    long long s = i0 + floor_sum(n - i0, G * KT, RT, RT * (i0 + 1) - 1 + G * (c + KT));
+    long long s = static_cast<long long>(COST) * n + i0 + floor_sum(n - i0, G * KT, RT, RT * (i0 + 1) - 1 + G * (c + KT));
     if (j > whole) s += units(a, q, whole);
     return s;
   }
@@ -153,11 +157,11 @@ __device__ __forceinline__ Line make_line(const AttnArgs& a, const Share& share,
   return line;
 }
 
-// A place in the line of units.
+// A place in the line.
 template <class S>
 struct Cursor {
   int r, h, j;         // item
-  int k, nu;           // unit in it, and its units
+  int k, nu;           // place in it, and its places (units and S::kCost)
   int nt;              // tiles of the request
   Request req;
   long long item0;     // the item's first unit in the line
