@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
   int* tok = tab_smem;            // [R + 1] first new token
   int* pag = tok + a.R + 1;       // [R + 1] first new page, from free_start
   int* len = pag + a.R + 1;       // [R] cached tokens; -1: refused
+  int* fresh = len + a.R;         // [R] new tokens, then new pages
   const int per = (a.R + kTabThreads - 1) / kTabThreads;
   const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
   const int P = 1 << a.log_page;
@@ -69,55 +70,58 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
   const bool lead = blockIdx.x == 0;
   if (threadIdx.x == 0) s_pages = 0;
 
+  // lengths come in whole lines, then each thread looks after `per` requests
+  for (int r = threadIdx.x; r < a.R; r += kTabThreads) {
+    len[r] = __ldg(a.kv_len + r);
+    fresh[r] = __ldg(a.new_len + r);
+  }
+  __syncthreads();
+
   // first new token of each request, cut at max_tokens
   long long sum = 0;
-  for (int r = r0; r < r1; ++r) sum += max(__ldg(a.new_len + r), 0);
-  long long at = block_scan(sum, part) - sum;
+  for (int r = r0; r < r1; ++r) sum += max(fresh[r], 0);
+  long long at = block_scan(sum, part) - sum, need_sum = 0;
   for (int r = r0; r < r1; ++r) {
+    const int kv = len[r], nw = fresh[r];
     tok[r] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
-    at += max(__ldg(a.new_len + r), 0);
-    const int kv = __ldg(a.kv_len + r), nw = __ldg(a.new_len + r);
-    const bool fits = kv >= 0 && nw >= 0 && static_cast<long long>(kv) + nw <= cap && at <= a.max_tokens;
-    len[r] = fits ? kv : -1;
+    at += max(nw, 0);
+    const long long end = static_cast<long long>(kv) + nw;
+    const bool fits = kv >= 0 && nw >= 0 && end <= cap && at <= a.max_tokens;
+    // new pages; -1: refused
+    fresh[r] = fits ? static_cast<int>(((end + P - 1) >> a.log_page) - ((static_cast<long long>(kv) + P - 1) >> a.log_page)) : -1;
+    need_sum += max(fresh[r], 0);
+    if (lead) a.kv_len_out[r] = fits ? static_cast<int>(end) : kv;  // unless pages run out
   }
   if (r0 < r1 && r1 == a.R) tok[a.R] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
 
   // first new page of each request
-  auto pages_of = [&](int r) -> int {
-    const int kv = len[r];
-    if (kv < 0) return 0;
-    const long long end = static_cast<long long>(kv) + __ldg(a.new_len + r);
-    return static_cast<int>(((end + P - 1) >> a.log_page) - ((static_cast<long long>(kv) + P - 1) >> a.log_page));
-  };
-  sum = 0;
-  for (int r = r0; r < r1; ++r) sum += pages_of(r);
-  at = block_scan(sum, part) - sum;
+  at = block_scan(need_sum, part) - need_sum;
   // free pages; a free_start outside [0, n_free] leaves none
   const long long have = start >= 0 && start <= a.n_free ? a.n_free - start : 0;
   int taken = 0;
   for (int r = r0; r < r1; ++r) {
-    const int need = pages_of(r);
+    const int need = fresh[r], kv = len[r];
     pag[r] = static_cast<int>(min(at, have));
-    at += need;
     if (need > 0) {
+      at += need;
       if (at <= have) taken = static_cast<int>(at);
-      else len[r] = -1;
     }
-    if (lead) {
-      const int kv = __ldg(a.kv_len + r);
-      const bool ok = len[r] >= 0;
-      a.kv_len_out[r] = ok ? kv + __ldg(a.new_len + r) : kv;
-      a.cu[r] = tok[r];
-      if (!ok) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_CAPACITY);
+    const bool ok = need == 0 || (need > 0 && at <= have);
+    if (!ok) {
+      len[r] = -1;
+      if (lead) {
+        a.kv_len_out[r] = kv;
+        atomicCAS(a.status, 0u, (unsigned)VSA_ERR_CAPACITY);
+      }
     }
   }
   if (r0 < r1 && r1 == a.R) pag[a.R] = static_cast<int>(min(at, have));
   if (taken > 0) atomicMax(&s_pages, taken);
   __syncthreads();
   const int pages = s_pages, tokens = tok[a.R];
-  if (lead && threadIdx.x == 0) {
-    a.cu[a.R] = tokens;
-    *a.free_next = start + pages;
+  if (lead) {
+    for (int r = threadIdx.x; r <= a.R; r += kTabThreads) a.cu[r] = tok[r];
+    if (threadIdx.x == 0) *a.free_next = start + pages;
   }
 
   // entries of the pages taken: page i of a request's new ones follows those it has
@@ -215,9 +219,10 @@ __global__ void __launch_bounds__(kTabThreads) cache_release_kernel(const uint8_
 //
 // A CTA takes 16 tokens x 2 heads: a warp holds 4 tokens of a head, 8 threads a
 // token, a thread one 16-channel block of its K and of its V (64 bytes in, 16
-// bytes of codes and 2 scales out).  The scale of a block is the thread's own
+// bytes of codes and 2 scales out).  Head pairs are the fast index of the grid:
+// CTAs that run together move the same tokens' rows.  The scale of a block is the thread's own
 // maximum, so nothing is exchanged but the 8 K scales of a token, which become
-// one store.  Tokens are the warp's fast index because 16 tokens of a head
+// two words.  Tokens are the warp's fast index because 16 tokens of a head
 // share a record: its lines are written from one CTA.
 // Bound: HBM (512 B in, 144 out a token and head).
 
@@ -225,8 +230,7 @@ constexpr int kPutThreads = 256;
 constexpr int kPutTokens = 16, kPutHeads = 2;
 
 template <bool F16>
-__device__ __forceinline__ void unpack16(const uint4* src, float (&f)[16]) {
-  const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+__device__ __forceinline__ void unpack16(uint4 w0, uint4 w1, float (&f)[16]) {
   const uint32_t wd[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -242,14 +246,20 @@ __device__ __forceinline__ void unpack16(const uint4* src, float (&f)[16]) {
 }
 
 // Codes of 16 values and their scale byte: s = E4M3(fl32(amax / 6)), code =
-// E2M1(fl32(x * fl32(1 / s))), the rounding of vsa_quantize_nvfp4.
-__device__ __forceinline__ uint2 quantise16(const float (&f)[16], uint32_t& sb) {
-  float amax = 0.0f;
+// E2M1(fl32(x * fl32(1 / s))), the rounding of vsa_quantize_nvfp4.  The quotient
+// by 6 is q = amax c, q + c (amax - 6 q) with c = fl32(1 / 6) (Markstein's
+// correction), which is the rounded one for every fp16 and bf16 amax between
+// 2^-20 and 2^20; below, s is 0 either way, and above 2688 it saturates, so
+// amax is cut at 3000.  `inverse` holds fl32(1 / s) of the 127 scales.
+__device__ __forceinline__ uint2 quantise16(const float (&f)[16], const float* inverse, uint32_t& sb) {
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-  sb = to_e4m3(__fdiv_rn(amax, 6.0f));
-  const float s = f16x2_to_f32(from_e4m3x2(sb)).x;
-  const float inv = s == 0.0f ? 0.0f : __frcp_rn(s);
+  for (int i = 0; i < 16; i += 2) m[(i >> 1) & 3] = max3f(m[(i >> 1) & 3], fabsf(f[i]), fabsf(f[i + 1]));
+  const float amax = fminf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), 3000.0f);
+  constexpr float c = 1.0f / 6.0f;
+  const float q = __fmul_rn(amax, c);
+  sb = to_e4m3(__fmaf_rn(__fmaf_rn(-6.0f, q, amax), c, q));
+  const float inv = inverse[sb];
   float y[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(f[i], inv);
@@ -259,24 +269,37 @@ __device__ __forceinline__ uint2 quantise16(const float (&f)[16], uint32_t& sb) 
 template <bool F16>
 __global__ void __launch_bounds__(kPutThreads) cache_append_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, long long k_stride, long long v_stride,
-    const int32_t* __restrict__ slots, int T, int Hkv, uint8_t* __restrict__ pages, int num_pages, int log_page,
-    unsigned int* status) {
+    const int32_t* __restrict__ slots, int T, int Hkv, int pairs, uint8_t* __restrict__ pages, int num_pages,
+    int log_page, unsigned int* status) {
   const int g = threadIdx.x & 7;  // 16-channel block
-  const int t = blockIdx.x * kPutTokens + ((threadIdx.x >> 3) & 15);
-  const int h = blockIdx.y * kPutHeads + (threadIdx.x >> 7);
+  const int group = blockIdx.x / pairs;
+  const int t = group * kPutTokens + ((threadIdx.x >> 3) & 15);
+  const int h = (blockIdx.x - group * pairs) * kPutHeads + (threadIdx.x >> 7);
   const bool in = t < T && h < Hkv;
   const int slot = in ? __ldg(slots + t) : -1;
   const bool bad = slot >= 0 && (slot >> log_page) >= num_pages;
   if (bad && g == 0) atomicCAS(status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
   const bool put = slot >= 0 && !bad;
+  __shared__ float inverse[128];
+  uint4 w[4];
+  if (put) {
+    const uint4* kp = reinterpret_cast<const uint4*>(k + t * k_stride + h * 128 + g * 16);
+    const uint4* vp = reinterpret_cast<const uint4*>(v + t * v_stride + h * 128 + g * 16);
+    w[0] = __ldg(kp), w[1] = __ldg(kp + 1), w[2] = __ldg(vp), w[3] = __ldg(vp + 1);
+  }
+  if (threadIdx.x < 128) {
+    const float s = f16x2_to_f32(from_e4m3x2(threadIdx.x)).x;
+    inverse[threadIdx.x] = s == 0.0f ? 0.0f : __frcp_rn(s);
+  }
+  __syncthreads();
   uint32_t ks = 0, vs = 0;
   uint2 kc = make_uint2(0, 0), vc = make_uint2(0, 0);
   if (put) {
     float f[16];
-    unpack16<F16>(reinterpret_cast<const uint4*>(k + t * k_stride + h * 128 + g * 16), f);
-    kc = quantise16(f, ks);
-    unpack16<F16>(reinterpret_cast<const uint4*>(v + t * v_stride + h * 128 + g * 16), f);
-    vc = quantise16(f, vs);
+    unpack16<F16>(w[0], w[1], f);
+    kc = quantise16(f, inverse, ks);
+    unpack16<F16>(w[2], w[3], f);
+    vc = quantise16(f, inverse, vs);
   }
   // a token's eight K scales as two words
   uint32_t word = ks;
@@ -292,51 +315,59 @@ __global__ void __launch_bounds__(kPutThreads) cache_append_kernel(
   rec[kRecVS + g * 16 + (p & 3) * 4 + (p >> 2)] = static_cast<uint8_t>(vs);
 }
 
+// Eight values from a word of codes and their scale byte.
 template <bool F16>
-__device__ __forceinline__ void store16(uint16_t* dst, uint2 codes, uint32_t sb) {
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sb) {
   const uint32_t s = dup_lo(from_e4m3x2(sb));
-  uint32_t r[8];
-  from_e2m1x8(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&r[0]));
-  from_e2m1x8(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&r[4]));
+  uint32_t r[4];
+  from_e2m1x8(codes, r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     r[i] = mul_f16x2(r[i], s);
     if (!F16) {
       const float2 x = f16x2_to_f32(r[i]);
       r[i] = pack_bf16x2(x.x, x.y);
     }
   }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// Read back: 16 threads a token and head, so that a store is one whole row; a
+// CTA takes 16 tokens x 2 heads, a thread one word of K and of V of both.
 template <bool F16>
 __global__ void __launch_bounds__(kPutThreads) cache_read_kernel(const int32_t* __restrict__ slots, int T, int Hkv,
-                                                                 const uint8_t* __restrict__ pages, int num_pages,
-                                                                 int log_page, uint16_t* __restrict__ k,
-                                                                 uint16_t* __restrict__ v, unsigned int* status) {
-  const int g = threadIdx.x & 7;
-  const int t = blockIdx.x * kPutTokens + ((threadIdx.x >> 3) & 15);
-  const int h = blockIdx.y * kPutHeads + (threadIdx.x >> 7);
-  if (t >= T || h >= Hkv) return;
+                                                                 int pairs, const uint8_t* __restrict__ pages,
+                                                                 int num_pages, int log_page, uint4* __restrict__ k,
+                                                                 uint4* __restrict__ v, unsigned int* status) {
+  const int x = threadIdx.x & 15, g = x >> 1;
+  const int group = blockIdx.x / pairs;
+  const int t = group * kPutTokens + (threadIdx.x >> 4);
+  const int h0 = (blockIdx.x - group * pairs) * kPutHeads;
+  if (t >= T) return;
   const int slot = __ldg(slots + t);
   if (slot < 0) return;
   if ((slot >> log_page) >= num_pages) {
-    if (g == 0) atomicCAS(status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+    if (x == 0) atomicCAS(status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
     return;
   }
   const int p = slot & 15;
-  const uint8_t* rec = pages + record_of(slot, h, Hkv, log_page);
-  const uint2 kc = __ldg(reinterpret_cast<const uint2*>(rec) + p * 8 + g);
-  const uint2 vc = __ldg(reinterpret_cast<const uint2*>(rec + kRecV) + p * 8 + g);
-  const uint32_t ks = __ldg(rec + kRecKS + p * 8 + g), vs = __ldg(rec + kRecVS + g * 16 + (p & 3) * 4 + (p >> 2));
-  const long long dst = (static_cast<long long>(t) * Hkv + h) * 128 + g * 16;
-  store16<F16>(k + dst, kc, ks);
-  store16<F16>(v + dst, vc, vs);
+#pragma unroll
+  for (int i = 0; i < kPutHeads; ++i) {
+    const int h = h0 + i;
+    if (h >= Hkv) break;
+    const uint8_t* rec = pages + record_of(slot, h, Hkv, log_page);
+    const uint32_t kc = __ldg(reinterpret_cast<const uint32_t*>(rec) + p * 16 + x);
+    const uint32_t vc = __ldg(reinterpret_cast<const uint32_t*>(rec + kRecV) + p * 16 + x);
+    const uint32_t ks = __ldg(rec + kRecKS + p * 8 + g), vs = __ldg(rec + kRecVS + g * 16 + (p & 3) * 4 + (p >> 2));
+    const long long dst = (static_cast<long long>(t) * Hkv + h) * 16 + x;
+    k[dst] = values8<F16>(kc, ks);
+    v[dst] = values8<F16>(vc, vs);
+  }
 }
 
-dim3 put_grid(int T, int Hkv) {
-  return dim3((T + kPutTokens - 1) / kPutTokens, (Hkv + kPutHeads - 1) / kPutHeads);
+int head_pairs(int Hkv) { return (Hkv + kPutHeads - 1) / kPutHeads; }
+long long put_grid(int T, int Hkv) {
+  return (static_cast<long long>(T) + kPutTokens - 1) / kPutTokens * head_pairs(Hkv);
 }
 
 }  // namespace
@@ -344,10 +375,10 @@ dim3 put_grid(int T, int Hkv) {
 cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStream_t stream) {
   const long long passes = (static_cast<long long>(a.max_tokens) + kTabSlots - 1) / kTabSlots;
   const int grid = static_cast<int>(passes < 1 ? 1 : passes < num_sms ? passes : num_sms);
-  const int smem = (3 * a.R + 2) * 4;
-  if (smem > 40 * 1024) {  // more than the default limit only for R > 3400
+  const int smem = (4 * a.R + 2) * 4;
+  if (smem > 40 * 1024) {  // more than the default limit only for R > 2559
     cudaError_t e = cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (3 * kMaxRequests + 2) * 4);
+                                         (4 * kMaxRequests + 2) * 4);
     if (e != cudaSuccess) return e;
   }
   cache_tables_kernel<<<grid, kTabThreads, smem, stream>>>(a);
@@ -366,17 +397,23 @@ cudaError_t launch_cache_append(bool f16, const uint16_t* k, const uint16_t* v, 
                                 long long v_stride, const int32_t* slots, int T, int Hkv, uint8_t* pages,
                                 int num_pages, int log_page, unsigned int* status, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
+  const long long grid = put_grid(T, Hkv);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = f16 ? cache_append_kernel<true> : cache_append_kernel<false>;
-  kern<<<put_grid(T, Hkv), kPutThreads, 0, stream>>>(k, v, k_stride, v_stride, slots, T, Hkv, pages, num_pages,
-                                                     log_page, status);
+  kern<<<static_cast<unsigned>(grid), kPutThreads, 0, stream>>>(k, v, k_stride, v_stride, slots, T, Hkv,
+                                                                head_pairs(Hkv), pages, num_pages, log_page, status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(bool f16, const int32_t* slots, int T, int Hkv, const uint8_t* pages, int num_pages,
                               int log_page, uint16_t* k, uint16_t* v, unsigned int* status, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
+  const long long grid = put_grid(T, Hkv);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = f16 ? cache_read_kernel<true> : cache_read_kernel<false>;
-  kern<<<put_grid(T, Hkv), kPutThreads, 0, stream>>>(slots, T, Hkv, pages, num_pages, log_page, k, v, status);
+  kern<<<static_cast<unsigned>(grid), kPutThreads, 0, stream>>>(slots, T, Hkv, head_pairs(Hkv), pages, num_pages,
+                                                                log_page, reinterpret_cast<uint4*>(k),
+                                                                reinterpret_cast<uint4*>(v), status);
   return cudaGetLastError();
 }
 

@@ -7,8 +7,11 @@
 // [0, 1] and the larger is 1, so the sum is in [1, 2]; a side of -inf gets
 // weight 0 and its o, which may be anything, is not read into the sum.
 // Bound: HBM (two 16-bit reads and one write a channel, 12 bytes a row).  One
-// CTA per (b, h, block) as in the plain untile; a thread owns one 16-byte
-// chunk of BS / 16 rows, all loaded before the first is used.
+// CTA per (64 tiled rows, b, h), heads the fast index, so that CTAs that run
+// together touch the same tokens' rows; a thread owns one 16-byte chunk of 4
+// rows, all loaded at once.  A row's weights are made by one lane for its 16
+// threads: with two exponentials, a logarithm and a quotient in every thread
+// the arithmetic took as long as the traffic (64 us for 306 MB, now LARGE).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,69 +31,75 @@ __device__ __forceinline__ float2 pair_of(uint32_t w) {
   return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
+constexpr int kMergeRows = 64;
+constexpr int kMergeIters = kMergeRows / (kTileThreads / kRowChunks);  // rows of a thread
+
 template <int BS, bool F16>
-__global__ void __launch_bounds__(kTileThreads) untile_merge_kernel(Geo g, int H, const uint4* __restrict__ ot,
+__global__ void __launch_bounds__(kTileThreads) untile_merge_kernel(Geo g, int H, int BH,
+                                                                    const uint4* __restrict__ ot,
                                                                     const float* __restrict__ lse_t,
                                                                     const uint4* past, const float* lse_past,
                                                                     uint4* o, float* lse) {
-  const int blk = blockIdx.x;
-  const int bh = blockIdx.y;
+  constexpr int kParts = BS / kMergeRows;
+  const int at = blockIdx.x / BH, bh = blockIdx.x - at * BH;
+  const int blk = at / kParts, first = (at - blk * kParts) * kMergeRows;
   const int b = bh / H, h = bh - b * H;
-  const int chunk = threadIdx.x & (kRowChunks - 1);
-  const int row0 = threadIdx.x >> 4;
-  constexpr int kIters = BS / 16;
-  constexpr int kBatch = kIters < 4 ? kIters : 4;  // rows in flight
-  const long long srow = static_cast<long long>(bh) * g.Sp + static_cast<long long>(blk) * BS;
-  const BlockOrigin org = block_origin(g, blk);
-#pragma unroll 1
-  for (int i0 = 0; i0 < kIters; i0 += kBatch) {
-    uint4 a[kBatch], c[kBatch];
-    float l1[kBatch], l2[kBatch];
-    long long dst[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int row = row0 + 16 * (i0 + i);
-      const long long s = token_of_slot(g, org, row);
-      dst[i] = s < 0 ? -1 : (static_cast<long long>(b) * g.S + s) * H + h;
-      a[i] = c[i] = make_uint4(0, 0, 0, 0);
-      l1[i] = l2[i] = 0.0f;
-      if (s >= 0) {
-        a[i] = __ldcs(ot + (srow + row) * kRowChunks + chunk);
-        c[i] = __ldcs(past + dst[i] * kRowChunks + chunk);
-        l1[i] = __ldg(lse_t + srow + row);
-        l2[i] = lse_past[dst[i]];
-      }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = lane & (kRowChunks - 1), upper = lane >> 4;
+  const long long srow = static_cast<long long>(bh) * g.Sp + static_cast<long long>(blk) * BS + first;
+
+  // lane 2 i + u looks after row 2 warp + u of the i-th 16: where it goes and its weights
+  long long dst = -1;
+  float l1 = 0.0f, l2 = 0.0f;
+  if (lane < 2 * kMergeIters) {
+    const int row = 2 * warp + (lane & 1) + 16 * (lane >> 1);
+    const long long s = token_of_slot(g, block_origin(g, blk), first + row);
+    if (s >= 0) {
+      dst = (static_cast<long long>(b) * g.S + s) * H + h;
+      l1 = __ldg(lse_t + srow + row);
+      l2 = lse_past[dst];
     }
-    __syncwarp();  // a row's 16 threads have read lse_past before one of them may overwrite it
+  }
+  uint4 x[kMergeIters], y[kMergeIters];
+  long long to[kMergeIters];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (dst[i] < 0) continue;
-      const float m = fmaxf(l1[i], l2[i]);
-      const bool none = m == -INFINITY;
-      const float w1 = l1[i] == -INFINITY ? 0.0f : expf(l1[i] - m);
-      const float w2 = l2[i] == -INFINITY ? 0.0f : expf(l2[i] - m);
-      const float sum = w1 + w2;
-      const float s1 = none ? 0.0f : w1 / sum, s2 = none ? 0.0f : w2 / sum;
-      const uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-      const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-      uint32_t r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = pair_of<F16>(aw[j]), y = pair_of<F16>(cw[j]);
-        float lo = 0.0f, hi = 0.0f;
-        if (w1 != 0.0f) {
-          lo = s1 * x.x;
-          hi = s1 * x.y;
-        }
-        if (w2 != 0.0f) {
-          lo = __fmaf_rn(s2, y.x, lo);
-          hi = __fmaf_rn(s2, y.y, hi);
-        }
-        r[j] = pack_half2<F16>(lo, hi);
-      }
-      __stcs(o + dst[i] * kRowChunks + chunk, make_uint4(r[0], r[1], r[2], r[3]));
-      if (lse != nullptr && chunk == 0) lse[dst[i]] = none ? -INFINITY : m + logf(sum);
+  for (int i = 0; i < kMergeIters; ++i) {
+    to[i] = __shfl_sync(0xffffffffu, dst, 2 * i + upper);
+    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+    if (to[i] >= 0) {
+      x[i] = __ldcs(ot + (srow + 2 * warp + upper + 16 * i) * kRowChunks + chunk);
+      y[i] = __ldcs(past + to[i] * kRowChunks + chunk);
     }
+  }
+  const float m = fmaxf(l1, l2);
+  const bool none = m == -INFINITY;
+  const float w1 = l1 == -INFINITY ? 0.0f : expf(l1 - m);
+  const float w2 = l2 == -INFINITY ? 0.0f : expf(l2 - m);
+  const float sum = w1 + w2;
+  const float s1 = none ? 0.0f : w1 / sum, s2 = none ? 0.0f : w2 / sum;
+  if (lse != nullptr && dst >= 0) lse[dst] = none ? -INFINITY : m + logf(sum);
+#pragma unroll
+  for (int i = 0; i < kMergeIters; ++i) {
+    const float a = __shfl_sync(0xffffffffu, s1, 2 * i + upper), c = __shfl_sync(0xffffffffu, s2, 2 * i + upper);
+    if (to[i] < 0) continue;
+    const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    const uint32_t yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = pair_of<F16>(xw[j]), q = pair_of<F16>(yw[j]);
+      float lo = 0.0f, hi = 0.0f;
+      if (a != 0.0f) {
+        lo = a * p.x;
+        hi = a * p.y;
+      }
+      if (c != 0.0f) {
+        lo = __fmaf_rn(c, q.x, lo);
+        hi = __fmaf_rn(c, q.y, hi);
+      }
+      r[j] = pack_half2<F16>(lo, hi);
+    }
+    __stcs(o + to[i] * kRowChunks + chunk, make_uint4(r[0], r[1], r[2], r[3]));
   }
 }
 
@@ -99,13 +108,14 @@ __global__ void __launch_bounds__(kTileThreads) untile_merge_kernel(Geo g, int H
 cudaError_t launch_untile_merge(const Geo& g, int B, int H, const uint16_t* ot, const float* lse_t,
                                 const uint16_t* past, const float* lse_past, uint16_t* o, float* lse, bool f16,
                                 cudaStream_t stream) {
-  dim3 grid(g.NB, B * H);
+  const long long grid = static_cast<long long>(g.NB) * (g.bs / kMergeRows) * B * H;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const uint4* oi = reinterpret_cast<const uint4*>(ot);
   const uint4* pi = reinterpret_cast<const uint4*>(past);
   uint4* oo = reinterpret_cast<uint4*>(o);
   auto kern = g.bs == 256 ? (f16 ? untile_merge_kernel<256, true> : untile_merge_kernel<256, false>)
                           : (f16 ? untile_merge_kernel<64, true> : untile_merge_kernel<64, false>);
-  kern<<<grid, kTileThreads, 0, stream>>>(g, H, oi, lse_t, pi, lse_past, oo, lse);
+  kern<<<static_cast<unsigned>(grid), kTileThreads, 0, stream>>>(g, H, B * H, oi, lse_t, pi, lse_past, oo, lse);
   return cudaGetLastError();
 }
 
