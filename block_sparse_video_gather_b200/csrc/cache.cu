@@ -43,12 +43,16 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part) {
   return v + before;
 }
 
+// Place of entry i of an array in shared memory: with 8 entries a thread (4096
+// requests) neighbouring threads start 9 words apart, in different banks.
+__host__ __device__ constexpr int spread(int i) { return i + (i >> 3); }
+
 // Largest i in [0, n) with a[i] <= x, given a[0] <= x.
 __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
+    if (a[spread(mid)] <= x) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -59,9 +63,10 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
   __shared__ long long part[kTabThreads / 32];
   __shared__ int s_pages;
   int* tok = tab_smem;            // [R + 1] first new token
-  int* pag = tok + a.R + 1;       // [R + 1] first new page, from free_start
-  int* len = pag + a.R + 1;       // [R] cached tokens; -1: refused
-  int* fresh = len + a.R;         // [R] new tokens, then new pages
+  const int words = spread(a.R) + 1;
+  int* pag = tok + words;         // [R + 1] first new page, from free_start
+  int* len = pag + words;         // [R] cached tokens; -1: refused
+  int* fresh = len + words;       // [R] new tokens, then new pages
   const int per = (a.R + kTabThreads - 1) / kTabThreads;
   const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
   const int P = 1 << a.log_page;
@@ -72,27 +77,27 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
 
   // lengths come in whole lines, then each thread looks after `per` requests
   for (int r = threadIdx.x; r < a.R; r += kTabThreads) {
-    len[r] = __ldg(a.kv_len + r);
-    fresh[r] = __ldg(a.new_len + r);
+    len[spread(r)] = __ldg(a.kv_len + r);
+    fresh[spread(r)] = __ldg(a.new_len + r);
   }
   __syncthreads();
 
   // first new token of each request, cut at max_tokens
   long long sum = 0;
-  for (int r = r0; r < r1; ++r) sum += max(fresh[r], 0);
+  for (int r = r0; r < r1; ++r) sum += max(fresh[spread(r)], 0);
   long long at = block_scan(sum, part) - sum, need_sum = 0;
   for (int r = r0; r < r1; ++r) {
-    const int kv = len[r], nw = fresh[r];
-    tok[r] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
+    const int kv = len[spread(r)], nw = fresh[spread(r)];
+    tok[spread(r)] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
     at += max(nw, 0);
     const long long end = static_cast<long long>(kv) + nw;
     const bool fits = kv >= 0 && nw >= 0 && end <= cap && at <= a.max_tokens;
     // new pages; -1: refused
-    fresh[r] = fits ? static_cast<int>(((end + P - 1) >> a.log_page) - ((static_cast<long long>(kv) + P - 1) >> a.log_page)) : -1;
-    need_sum += max(fresh[r], 0);
+    fresh[spread(r)] = fits ? static_cast<int>(((end + P - 1) >> a.log_page) - ((static_cast<long long>(kv) + P - 1) >> a.log_page)) : -1;
+    need_sum += max(fresh[spread(r)], 0);
     if (lead) a.kv_len_out[r] = fits ? static_cast<int>(end) : kv;  // unless pages run out
   }
-  if (r0 < r1 && r1 == a.R) tok[a.R] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
+  if (r0 < r1 && r1 == a.R) tok[spread(a.R)] = static_cast<int>(min(at, static_cast<long long>(a.max_tokens)));
 
   // first new page of each request
   at = block_scan(need_sum, part) - need_sum;
@@ -100,35 +105,35 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
   const long long have = start >= 0 && start <= a.n_free ? a.n_free - start : 0;
   int taken = 0;
   for (int r = r0; r < r1; ++r) {
-    const int need = fresh[r], kv = len[r];
-    pag[r] = static_cast<int>(min(at, have));
+    const int need = fresh[spread(r)], kv = len[spread(r)];
+    pag[spread(r)] = static_cast<int>(min(at, have));
     if (need > 0) {
       at += need;
       if (at <= have) taken = static_cast<int>(at);
     }
     const bool ok = need == 0 || (need > 0 && at <= have);
     if (!ok) {
-      len[r] = -1;
+      len[spread(r)] = -1;
       if (lead) {
         a.kv_len_out[r] = kv;
         atomicCAS(a.status, 0u, (unsigned)VSA_ERR_CAPACITY);
       }
     }
   }
-  if (r0 < r1 && r1 == a.R) pag[a.R] = static_cast<int>(min(at, have));
+  if (r0 < r1 && r1 == a.R) pag[spread(a.R)] = static_cast<int>(min(at, have));
   if (taken > 0) atomicMax(&s_pages, taken);
   __syncthreads();
-  const int pages = s_pages, tokens = tok[a.R];
+  const int pages = s_pages, tokens = tok[spread(a.R)];
   if (lead) {
-    for (int r = threadIdx.x; r <= a.R; r += kTabThreads) a.cu[r] = tok[r];
+    for (int r = threadIdx.x; r <= a.R; r += kTabThreads) a.cu[r] = tok[spread(r)];
     if (threadIdx.x == 0) *a.free_next = start + pages;
   }
 
   // entries of the pages taken: page i of a request's new ones follows those it has
   for (int e = blockIdx.x * kTabThreads + threadIdx.x; e < pages; e += gridDim.x * kTabThreads) {
     const int r = last_at_most(pag, a.R, e);
-    const int had = (len[r] + P - 1) >> a.log_page;
-    a.table[static_cast<long long>(r) * a.max_pages + had + (e - pag[r])] = __ldg(a.free_pages + start + e);
+    const int had = (len[spread(r)] + P - 1) >> a.log_page;
+    a.table[static_cast<long long>(r) * a.max_pages + had + (e - pag[spread(r)])] = __ldg(a.free_pages + start + e);
   }
 
   // slots; a token of a page taken now reads its id from the stack, not from the entry above
@@ -138,17 +143,27 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
     int4 out = make_int4(-1, -1, -1, -1);
     int* ov = &out.x;
     int r = i0 < tokens ? last_at_most(tok, a.R, static_cast<int>(i0)) : 0;
+    int known_r = -1, known_pi = -1, page = -1;  // neighbours are mostly in one page
     for (int j = 0; j < 4; ++j) {
       const int i = static_cast<int>(i0) + j;
       if (i >= tokens) break;
-      while (tok[r + 1] <= i) ++r;  // ends: tok[R] = tokens > i
-      if (len[r] < 0) continue;
-      const int pos = len[r] + (i - tok[r]);
-      const int pi = pos >> a.log_page, had = (len[r] + P - 1) >> a.log_page;
-      const int page = pi < had ? __ldg(a.table + static_cast<long long>(r) * a.max_pages + pi)
-                                : __ldg(a.free_pages + start + pag[r] + (pi - had));
-      if (page < 0 || page >= page_limit) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
-      else ov[j] = (page << a.log_page) + (pos & (P - 1));
+      while (tok[spread(r + 1)] <= i) ++r;  // ends: tok[R] = tokens > i
+      const int kv = len[spread(r)];
+      if (kv < 0) continue;
+      const int pos = kv + (i - tok[spread(r)]);
+      const int pi = pos >> a.log_page;
+      if (r != known_r || pi != known_pi) {
+        known_r = r;
+        known_pi = pi;
+        const int had = (kv + P - 1) >> a.log_page;
+        page = pi < had ? __ldg(a.table + static_cast<long long>(r) * a.max_pages + pi)
+                        : __ldg(a.free_pages + start + pag[spread(r)] + (pi - had));
+        if (page < 0 || page >= page_limit) {
+          atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+          page = -1;
+        }
+      }
+      if (page >= 0) ov[j] = (page << a.log_page) + (pos & (P - 1));
     }
     if (i0 + 4 <= a.max_tokens) {
       *reinterpret_cast<int4*>(a.slots + i0) = out;
@@ -198,15 +213,15 @@ __global__ void __launch_bounds__(kTabThreads) cache_release_kernel(const uint8_
   }
   long long at = incl - sum;
   for (int r = r0; r < r1; ++r) {
-    pag[r] = static_cast<int>(at);
+    pag[spread(r)] = static_cast<int>(at);
     at += pages_of(r);
   }
-  if (threadIdx.x == 0) pag[R] = static_cast<int>(m);
+  if (threadIdx.x == 0) pag[spread(R)] = static_cast<int>(m);
   __syncthreads();
   const int base = start - static_cast<int>(m);
   for (int e = threadIdx.x; e < static_cast<int>(m); e += kTabThreads) {
     const int r = last_at_most(pag, R, e);
-    free_pages[base + e] = table[static_cast<long long>(r) * max_pages + (e - pag[r])];
+    free_pages[base + e] = table[static_cast<long long>(r) * max_pages + (e - pag[spread(r)])];
   }
   for (int r = r0; r < r1; ++r)
     if (drop[r]) kv_len[r] = 0;
@@ -375,10 +390,10 @@ long long put_grid(int T, int Hkv) {
 cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStream_t stream) {
   const long long passes = (static_cast<long long>(a.max_tokens) + kTabSlots - 1) / kTabSlots;
   const int grid = static_cast<int>(passes < 1 ? 1 : passes < num_sms ? passes : num_sms);
-  const int smem = (4 * a.R + 2) * 4;
-  if (smem > 40 * 1024) {  // more than the default limit only for R > 2559
+  const int smem = 4 * (spread(a.R) + 1) * 4;
+  if (smem > 40 * 1024) {  // more than the default limit only for R > 2275
     cudaError_t e = cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * kMaxRequests + 2) * 4);
+                                         4 * (spread(kMaxRequests) + 1) * 4);
     if (e != cudaSuccess) return e;
   }
   cache_tables_kernel<<<grid, kTabThreads, smem, stream>>>(a);
@@ -388,7 +403,7 @@ cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStrea
 cudaError_t launch_cache_release(const uint8_t* drop, int R, int log_page, int32_t* kv_len, const int32_t* table,
                                  int max_pages, int32_t* free_pages, int n_free, int32_t* free_start,
                                  unsigned int* status, cudaStream_t stream) {
-  cache_release_kernel<<<1, kTabThreads, (R + 1) * 4, stream>>>(drop, R, log_page, kv_len, table, max_pages,
+  cache_release_kernel<<<1, kTabThreads, (spread(R) + 1) * 4, stream>>>(drop, R, log_page, kv_len, table, max_pages,
                                                                 free_pages, n_free, free_start, status);
   return cudaGetLastError();
 }
