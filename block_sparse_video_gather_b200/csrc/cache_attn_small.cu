@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(W * 32, 1)
   const long long U = line.total;
   if (U == 0) return;
   const long long wanted = (U + W * kMinUnits - 1) / (W * kMinUnits);
-  const int N = wanted < gridDim.x ? static_cast<int>(wanted) : static_cast<int>(gridDim.x);
+  int N = wanted < gridDim.x ? static_cast<int>(wanted) : static_cast<int>(gridDim.x);
+  // a batch that does not fill the GPU: whole CTAs for an item, so that items of one length need no joining between CTAs
+  if (N < static_cast<int>(gridDim.x) && line.items > 0 && N > line.items) N -= N % line.items;
   const int cta = blockIdx.x;
   if (cta >= N) return;
   const Cut cut(U, N);
@@ -507,14 +509,18 @@ __global__ void __launch_bounds__(W * 32, 1)
   constexpr size_t kPart = part_floats<RT>();
   const long long key = lane < 2 * W ? sm.meta[lane].item0 : -1;
   const float* mine_at = reinterpret_cast<const float*>(lane & 1 ? &sm.ring[lane / 2 % W][0][0] : &sm.piece[lane / 2 % W][0]);
-  const unsigned alike = __match_any_sync(0xffffffffu, key);
-  unsigned leaders = __ballot_sync(0xffffffffu, key >= 0 && __ffs(alike) - 1 == lane);
+  // the pieces are in the order of the line: an item's are neighbours among those that are there
+  const unsigned there = __ballot_sync(0xffffffffu, key >= 0);
+  const unsigned below = there & ((1u << lane) - 1);
+  const long long before = __shfl_sync(0xffffffffu, key, below ? 31 - __clz(below) : lane);
+  unsigned leaders = __ballot_sync(0xffffffffu, key >= 0 && (below == 0 || before != key));
   PieceMeta cross[2];  // items that go beyond the CTA: begun before it, going on after it
   cross[0].item0 = cross[1].item0 = -1;
   while (leaders) {
     const int lead = __ffs(leaders) - 1;
     leaders &= leaders - 1;
-    const unsigned group = __shfl_sync(0xffffffffu, alike, lead);
+    // from the leader to the next
+    const unsigned group = there & (~0u << lead) & (leaders ? (leaders & -leaders) - 1 : ~0u);
     const PieceMeta mt = sm.meta[lead];
     const bool whole = mt.item0 >= cs && mt.item0 + mt.nu <= ce;
     const int slot = mt.item0 < cs ? 0 : 1;

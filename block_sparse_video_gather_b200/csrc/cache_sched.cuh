@@ -87,8 +87,17 @@ __device__ __forceinline__ bool takes(const Share& s, const AttnArgs& a, const R
 // one array of sums in shared memory, made by the whole CTA.
 struct Line {
   long long total;     // U
+  int items;           // (request, key head, tile)s where known (R <= 32), else 0
   long long at, units; // lane r: first unit and units of request r (R <= 32)
+  Request own;         // lane r: request r (R <= 32)
   const long long* pre;  // [R + 1] first units (R > 32)
+
+  // Request r.  All lanes of a warp, r the same in all.
+  __device__ __forceinline__ Request request(const AttnArgs& a, int r) const {
+    if (a.R > 32) return load_request(a, r, false);
+    return Request{__shfl_sync(0xffffffffu, own.q0, r), __shfl_sync(0xffffffffu, own.n, r),
+                   __shfl_sync(0xffffffffu, own.kv, r)};
+  }
 
   // The request that holds unit u < U, and its first unit.  All lanes of a warp.
   __device__ __forceinline__ int request_of(int R, long long u, long long& first) const {
@@ -126,14 +135,23 @@ __device__ __forceinline__ Line make_line(const AttnArgs& a, const Share& share,
   Line line;
   line.pre = pre;
   line.at = line.units = 0;
+  line.items = 0;
+  line.own = Request{0, 0, 0};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto units_of = [&](int r, bool report) -> long long {
     const Request q = load_request(a, r, report);
     return takes(share, a, q) ? S::units_before(a, q, S::tiles(a, q)) * a.Hkv : 0;
   };
   if (a.R <= 32) {
-    if (lane < a.R) line.units = units_of(lane, blockIdx.x == 0 && warp == 0);
+    if (lane < a.R) {
+      line.own = load_request(a, lane, blockIdx.x == 0 && warp == 0);
+      if (takes(share, a, line.own)) {
+        line.items = S::tiles(a, line.own);
+        line.units = S::units_before(a, line.own, line.items) * a.Hkv;
+      }
+    }
     const long long v = warp_scan(line.units);
+    line.items = __reduce_add_sync(0xffffffffu, line.items) * a.Hkv;
     line.at = v - line.units;
     line.total = __shfl_sync(0xffffffffu, v, 31);
     return line;
@@ -170,20 +188,26 @@ struct Cursor {
   __device__ __forceinline__ void seek(const AttnArgs& a, const Line& line, long long u) {
     long long first;
     r = line.request_of(a.R, u, first);
-    req = load_request(a, r, false);
+    req = line.request(a, r);
     nt = S::tiles(a, req);
     const long long head = S::units_before(a, req, nt);
     long long rem = u - first;
     h = static_cast<int>(div_small(rem, head));
     rem -= h * head;
     int tl = 0, th = nt;
+    long long before = 0;
     while (th - tl > 1) {
       const int mid = (tl + th) >> 1;
-      if (S::units_before(a, req, mid) <= rem) tl = mid;
-      else th = mid;
+      const long long x = S::units_before(a, req, mid);
+      if (x <= rem) {
+        tl = mid;
+        before = x;
+      } else {
+        th = mid;
+      }
     }
     j = tl;
-    k = static_cast<int>(rem - S::units_before(a, req, j));
+    k = static_cast<int>(rem - before);
     nu = S::units(a, req, j);
     item0 = u - k;
   }
