@@ -10,7 +10,7 @@ constexpr int kWorkers = 160;  // CTAs of a call at most: one per SM, B200 has 1
 
 // Requests of up to this many rows (new tokens times query heads of a key head)
 // run the kernel for few rows, others the 256-row tiles of the tensor cores.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 48;
 
 }  // namespace
 

@@ -42,6 +42,7 @@ using namespace cache;
 constexpr int kUnit = 32;                        // keys of a unit: two records
 constexpr int kUnitBytes = 2 * kRecBytes;
 constexpr uint64_t kTimeoutNs = 2000000000ull;   // 2 s per wait
+constexpr int kAtOnce = 16;                      // parts of a row that a warp loads at once when it joins them
 constexpr int kMinUnits = 2;                     // units a warp gets at least
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -239,8 +240,6 @@ __global__ void __launch_bounds__(W * 32, 1)
         head_base = a.pages + (static_cast<long long>(lc.h) * kRecBytes << log_rec);
       }
     };
-    for (int i = 0; i < STAGES && i < total; ++i) issue(i);
-
     uint32_t qf[NT][16];
     float rs[NT][2], m[NT][2], l[NT][2], base[NT][2];  // base: -m, or 0 where there is none yet
     int lim[NT][2];
@@ -250,31 +249,38 @@ __global__ void __launch_bounds__(W * 32, 1)
     int s = 0;
     uint32_t parity = 0;
 
+    // the rows of q of the item at cc: thread (g, c) channels 32 c .. 32 c + 31 of row g
+    auto load_q = [&]() {
+      const int rows = cc.req.n * a.G;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = cc.j * RT + n * 8 + g;
+        const int token = row / a.G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (static_cast<long long>(cc.req.q0) + token) * a.q_stride + (cc.h * a.G + row - token * a.G) * 128 +
+            c * 32);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (row < rows) w = __ldg(src + x);
+          qf[n][4 * x] = w.x, qf[n][4 * x + 1] = w.y, qf[n][4 * x + 2] = w.z, qf[n][4 * x + 3] = w.w;
+        }
+      }
+    };
+    load_q();  // on its way while the first records are found
+    for (int i = 0; i < STAGES && i < total; ++i) issue(i);
+
     for (int i = 0; i < total; ++i) {
       if (i == 0 || cc.k == 0) {
-        // ---- a new item: its rows of q as B fragments, thread (g, c) channels 32 c .. 32 c + 31 of row g
+        // ---- a new item: its rows of q as B fragments
+        if (i > 0) load_q();
         from_start = cc.k == 0;
         const int rows = cc.req.n * a.G;
         lim_min = visible(a, cc.req, cc.j * RT / a.G);
         seen = S::keys(a, cc.req, cc.j);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const int row = cc.j * RT + n * 8 + g;
-          const int token = row / a.G;
           float amax = 0.0f;
-          if (row < rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + (static_cast<long long>(cc.req.q0) + token) * a.q_stride + (cc.h * a.G + row - token * a.G) * 128 +
-                c * 32);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint4 w = __ldg(src + x);
-              qf[n][4 * x] = w.x, qf[n][4 * x + 1] = w.y, qf[n][4 * x + 2] = w.z, qf[n][4 * x + 3] = w.w;
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) qf[n][x] = 0u;
-          }
           float inv = 1.0f;
           if (!F16) {
 #pragma unroll
@@ -572,16 +578,18 @@ __global__ void __launch_bounds__(W * 32, 1)
       t.m = -INFINITY;
       t.l = 0.0f;
       t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int w0 = first; w0 <= last; w0 += 32) {
-        const bool in = w0 + lane <= last;
-        const float* f = part_of(in ? w0 + lane : last);
-        RowPart u = join_weights(in ? __ldcg(f + RT * 128 + row) : -INFINITY, in ? __ldcg(f + RT * 129 + row) : 0.0f);
-        const int n = min(32, last - w0 + 1);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i)
-          add_part(u, __ldcg(reinterpret_cast<const float4*>(part_of(w0 + i) + row * 128) + lane),
-                   __shfl_sync(0xffffffffu, u.w, i));
-        // the 32 parts' sum joins those before it
+      for (int w0 = first; w0 <= last; w0 += kAtOnce) {
+        const int n = min(kAtOnce, last - w0 + 1);
+        float4 o[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          o[i] = i < n ? __ldcg(reinterpret_cast<const float4*>(part_of(w0 + i) + row * 128) + lane)
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float* f = part_of(w0 + min(lane, n - 1));
+        RowPart u = join_weights(lane < n ? __ldcg(f + RT * 128 + row) : -INFINITY, lane < n ? __ldcg(f + RT * 129 + row) : 0.0f);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) add_part(u, o[i], __shfl_sync(0xffffffffu, u.w, i));
+        // their sum joins those before it
         const float m = fmaxf(t.m, u.m), wt = part_weight(t.m, m), wu = part_weight(u.m, m);
         t.o = make_float4(wt * t.o.x + wu * u.o.x, wt * t.o.y + wu * u.o.y, wt * t.o.z + wu * u.o.z,
                           wt * t.o.w + wu * u.o.w);
