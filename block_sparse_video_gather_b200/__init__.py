@@ -511,24 +511,23 @@ def _at(t, dtype, dev, what):
     raise ValueError(f"{what} must be contiguous")
 
 
-def _rows(t, what):
-    """A [T, heads, 128] tensor whose tokens may be strided (a slice of a fused projection):
-    (pointer, elements from token to token)."""
-    if t.dim() != 3 or t.shape[2] != 128:
-        raise ValueError(f"{what} must be [tokens, heads, 128], got {tuple(t.shape)}")
-    T, H, D = t.shape
+def _row_stride(t, shape, what):
+    """Elements from token to token of a [T, heads, 128] tensor (its shape) whose tokens may be strided (a slice of a
+    fused projection)."""
+    if len(shape) != 3 or shape[2] != 128:
+        raise ValueError(f"{what} must be [tokens, heads, 128], got {tuple(shape)}")
     st = t.stride()
-    if st[2] != 1 or (H > 1 and st[1] != D):
+    if st[2] != 1 or (st[1] != 128 and shape[1] > 1):
         raise ValueError(f"{what}: heads and channels must be contiguous")
-    return t.data_ptr(), (st[0] if T > 1 else max(st[0], H * D) & ~7)
+    return st[0] if shape[0] > 1 else shape[1] * 128
 
 
 def _pages_shape(pages):
     """(num_pages, Hkv, page_tokens) of a cache's pages [num_pages, Hkv, page_tokens / 16, 2304]."""
-    if pages.dim() != 4 or pages.shape[3] != CACHE_RECORD_BYTES:
-        raise ValueError(f"pages must be [num_pages, Hkv, page_tokens / 16, {CACHE_RECORD_BYTES}], got "
-                         f"{tuple(pages.shape)}")
-    return pages.shape[0], pages.shape[1], pages.shape[2] * 16
+    s = pages.shape
+    if len(s) != 4 or s[3] != CACHE_RECORD_BYTES:
+        raise ValueError(f"pages must be [num_pages, Hkv, page_tokens / 16, {CACHE_RECORD_BYTES}], got {tuple(s)}")
+    return s[0], s[1], s[2] * 16
 
 
 def cache_pages(num_pages: int, Hkv: int, page_tokens: int = 64, device="cuda", D: int = 128):
@@ -545,8 +544,9 @@ def cache_tables(kv_len, new_len, page_tokens: int, free_pages, free_start, bloc
     [R, max_pages] and the new tokens' slots (all of `slots`; -1 past the last), and returns (kv_len_out [R],
     cu [R + 1], free_next [1]).  See vsa_cache_tables; kv_len_out and free_next must be other tensors than kv_len
     and free_start."""
-    R = kv_len.shape[0]
-    if kv_len.shape != (R,) or new_len.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
+    R = kv_len.numel()
+    rows, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    if kv_len.dim() != 1 or new_len.dim() != 1 or new_len.numel() != R or rows != R:
         raise ValueError("kv_len and new_len must be [R], block_table [R, max_pages]")
     dev, stream = _device_and_stream(kv_len, "kv_len")
     torch = _torch_module
@@ -562,7 +562,7 @@ def cache_tables(kv_len, new_len, page_tokens: int, free_pages, free_start, bloc
     _check(lib().vsa_cache_tables(
         _at(kv_len, i32, dev, "kv_len"), _at(new_len, i32, dev, "new_len"), R, page_tokens,
         _at(free_pages, i32, dev, "free_pages"), free_pages.numel(), _at(free_start, i32, dev, "free_start"),
-        _at(block_table, i32, dev, "block_table"), block_table.shape[1], _at(kv_len_out, i32, dev, "kv_len_out"),
+        _at(block_table, i32, dev, "block_table"), max_pages, _at(kv_len_out, i32, dev, "kv_len_out"),
         _at(cu_out, i32, dev, "cu_out"), _at(slots, i32, dev, "slots"), slots.numel(),
         _at(free_next_out, i32, dev, "free_next_out"), stream), "vsa_cache_tables")
     return kv_len_out, cu_out, free_next_out
@@ -588,44 +588,49 @@ def cache_append(k, v, slots, pages):
     (negative: not written)."""
     n, Hkv, page_tokens = _pages_shape(pages)
     code = _dtype_code(k, "k")
-    if v.dtype != k.dtype or v.shape != k.shape or k.dim() != 3 or k.shape[1] != Hkv:
-        raise ValueError(f"k and v must be [T, {Hkv}, 128] of one type, got {tuple(k.shape)} and {tuple(v.shape)}")
-    T, _, D = k.shape
-    if slots.shape != (T,):
+    shape = k.shape
+    if v.dtype != k.dtype or v.shape != shape or len(shape) != 3 or shape[1] != Hkv:
+        raise ValueError(f"k and v must be [T, {Hkv}, 128] of one type, got {tuple(shape)} and {tuple(v.shape)}")
+    T = shape[0]
+    if slots.dim() != 1 or slots.numel() != T:
         raise ValueError(f"slots must be [{T}], got {tuple(slots.shape)}")
     if T == 0:
         return
     dev, stream = _device_and_stream(pages, "pages")
     if k.get_device() != dev or v.get_device() != dev:
         raise ValueError(f"k and v must be on cuda:{dev}")
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v")
-    _check(lib().vsa_cache_append_nvfp4(code, kp, vp, ks, vs, _at(slots, _torch_module.int32, dev, "slots"), T, Hkv, D,
-                                        _at(pages, _torch_module.uint8, dev, "pages"), n, page_tokens, stream),
-           "vsa_cache_append_nvfp4")
+    _check(lib().vsa_cache_append_nvfp4(
+        code, k.data_ptr(), v.data_ptr(), _row_stride(k, shape, "k"), _row_stride(v, shape, "v"),
+        _at(slots, _torch_module.int32, dev, "slots"), T, Hkv, 128, _at(pages, _torch_module.uint8, dev, "pages"), n,
+        page_tokens, stream), "vsa_cache_append_nvfp4")
 
 
 def cache_read(slots, pages, dtype=None, k_out=None, v_out=None):
     """The cached keys and values at the slots -> (k, v) [T, Hkv, 128]; rows of negative slots are left as they
     were (zero in tensors made here)."""
-    torch = _torch()
     n, Hkv, page_tokens = _pages_shape(pages)
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
-    T = slots.shape[0]
-    dtype = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
-    if k_out is None:
-        k_out = torch.zeros((T, Hkv, 128), dtype=dtype, device=pages.device)
-    if v_out is None:
-        v_out = torch.zeros((T, Hkv, 128), dtype=dtype, device=pages.device)
+    T = slots.numel()
+    if k_out is None or v_out is None:
+        torch = _torch()
+        dtype = dtype or (k_out if k_out is not None else v_out if v_out is not None else pages.new_empty(
+            0, dtype=torch.bfloat16)).dtype
+        if k_out is None:
+            k_out = torch.zeros((T, Hkv, 128), dtype=dtype, device=pages.device)
+        if v_out is None:
+            v_out = torch.zeros((T, Hkv, 128), dtype=dtype, device=pages.device)
+    dtype = k_out.dtype
+    code = _dtype_code(k_out, "k_out")
     if k_out.shape != (T, Hkv, 128) or v_out.shape != (T, Hkv, 128):
         raise ValueError(f"k_out and v_out must be [{T}, {Hkv}, 128]")
     if T == 0:
         return k_out, v_out
     dev, stream = _device_and_stream(pages, "pages")
-    _check(lib().vsa_cache_read_nvfp4(_dtype_code(k_out, "k_out"), _at(slots, torch.int32, dev, "slots"), T, Hkv, 128,
-                                      _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(k_out, dtype, dev, "k_out"),
-                                      _at(v_out, dtype, dev, "v_out"), stream), "vsa_cache_read_nvfp4")
+    _check(lib().vsa_cache_read_nvfp4(
+        code, _at(slots, _torch_module.int32, dev, "slots"), T, Hkv, 128,
+        _at(pages, _torch_module.uint8, dev, "pages"), n, page_tokens, _at(k_out, dtype, dev, "k_out"),
+        _at(v_out, dtype, dev, "v_out"), stream), "vsa_cache_read_nvfp4")
     return k_out, v_out
 
 
@@ -650,10 +655,12 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
     torch = _torch_module
     n, Hkv, page_tokens = _pages_shape(pages)
     code = _dtype_code(q, "q")
-    qp, qs = _rows(q, "q")
-    T, Hq, D = q.shape
-    R = kv_len.shape[0]
-    if cu.shape != (R + 1,) or block_table.dim() != 2 or block_table.shape[0] != R:
+    shape = q.shape
+    qs = _row_stride(q, shape, "q")
+    T, Hq, D = shape
+    R = kv_len.numel()
+    rows, max_pages = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    if kv_len.dim() != 1 or cu.dim() != 1 or cu.numel() != R + 1 or rows != R:
         raise ValueError("kv_len must be [R], cu [R + 1], block_table [R, max_pages]")
     need = _attn_workspace_bytes(Hq, Hkv, max_q)
     if workspace.numel() * workspace.element_size() < need:
@@ -662,15 +669,15 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
         o_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
     if lse_out is None:
         lse_out = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    if o_out.shape != (T, Hq, D) or lse_out.shape != (T, Hq):
+    if o_out.shape != shape or lse_out.shape != shape[:2]:
         raise ValueError(f"o_out must be [{T}, {Hq}, {D}], lse_out [{T}, {Hq}]")
     if T == 0:
         return o_out, lse_out
     i32 = torch.int32
     _check(lib().vsa_cache_attn_nvfp4(
-        code, qp, qs, _at(cu, i32, dev, "cu"), _at(kv_len, i32, dev, "kv_len"), R, T, max_q, Hq, Hkv, D,
+        code, q.data_ptr(), qs, _at(cu, i32, dev, "cu"), _at(kv_len, i32, dev, "kv_len"), R, T, max_q, Hq, Hkv, D,
         _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(block_table, i32, dev, "block_table"),
-        block_table.shape[1], int(causal), _at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
+        max_pages, int(causal), _at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
         _at(workspace, workspace.dtype, dev, "workspace"), stream), "vsa_cache_attn_nvfp4")
     return o_out, lse_out
 
