@@ -327,6 +327,56 @@ def test_attention_over_long_caches(n, kv, Hq, Hkv, page):
     b.check(*b.run(False), False)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,kv", [([1] * 50, [0, 1, 40, 90] * 12 + [7, 16]), ([60, 2, 0, 1] * 11, [60, 130, 5, 0] * 11),
+                                  ([100], [0]), ([70, 70], [0, 33])])
+def test_attention_of_many_requests_and_of_empty_ones(n, kv, causal):
+    """More requests than a warp has lanes, on either kernel and on both, and requests without a cached token."""
+    b = Batch(n, kv, 2, 1, 16, "f16", pad_rows=1)
+    b.check(*b.run(causal), causal)
+
+
+def test_attention_of_the_most_requests():
+    R = 4096
+    rng = np.random.default_rng(9)
+    b = Batch([1] * R, list(rng.integers(0, 40, R)), 1, 1, 16, "bf16")
+    b.check(*b.run(True), True)
+    n = [1] * R
+    n[7], n[4095] = 70, 50
+    b = Batch(n, list(np.maximum(n, rng.integers(0, 40, R))), 1, 1, 16, "bf16")
+    b.check(*b.run(True), True)
+
+
+@pytest.mark.parametrize("n", [1, 64])
+def test_attention_after_a_workspace_that_was_not_zero(n):
+    """Counters that were not zero join an item early or not at all -- wrong rows, no hang -- and once the workspace
+    is zeroed again the results are right."""
+    b = Batch([n], [6000], 1, 1, 64, "bf16")
+    good = b.run(False)
+    b.ws.view(torch.int32)[:1024] = 5
+    b.run(False)
+    b.ws.zero_()
+    o, lse = b.run(False)
+    assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_append_of_every_scale(dtype):
+    """Blocks whose largest value makes each of E4M3's scales, and values at the borders between codes."""
+    x = np.zeros((127, 1, 128), np.float32)
+    steps = np.array([0.25, 0.5, 0.75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 5.5, 6], np.float32)
+    for b in range(127):
+        x[b, 0, 0:15] = steps * F.E4M3[b]
+        x[b, 0, 16:31] = -steps * F.E4M3[b]
+        x[b, 0, 32:128] = np.random.default_rng(b).uniform(-6, 6, 96) * F.E4M3[b]
+    k = torch.from_numpy(x).to(TDT[dtype]).cuda()
+    pages = torch.zeros((8, 1, 1, F.REC), dtype=torch.uint8, device="cuda")
+    vsa.cache_append(k, -k, i32(np.arange(127)), pages)
+    want = np.zeros((8, 1, 1, F.REC), np.uint8)
+    F.put(want, np.arange(127), f64(k), f64(-k))
+    np.testing.assert_array_equal(pages.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-3, 30.0, 3e4])
 @pytest.mark.parametrize("n", [1, 100])
 def test_attention_of_small_and_large_queries(scale, n):
