@@ -22,7 +22,9 @@ using namespace cache;
 // itself in shared memory -- R <= 4096 lengths are 32 KB out of L2 -- and then
 // fills its share of the slots and of the new table entries, finding the
 // request by bisection; so the call is one launch with nothing to wait for.
-// The bound is latency: the largest call writes some MB.
+// The bound is latency: the largest call writes some MB.  8 requests 4.6 us, 4096
+// requests with 1.02 M new tokens 14 us, of which the slots take 7 (four CTAs'
+// worth of passes side by side, or eight tokens a thread, were slower).
 
 constexpr int kTabThreads = 512;
 constexpr int kTabSlots = kTabThreads * 4;  // slots of one pass of a CTA
@@ -239,7 +241,8 @@ __global__ void __launch_bounds__(kTabThreads) cache_release_kernel(const uint8_
 // maximum, so nothing is exchanged but the 8 K scales of a token, which become
 // two words.  Tokens are the warp's fast index because 16 tokens of a head
 // share a record: its lines are written from one CTA.
-// Bound: HBM (512 B in, 144 out a token and head).
+// Bound: HBM (512 B in, 144 out a token and head).  27280 tokens x 24 heads: append
+// 72 us and read back 74 us for 430 MB each, 6.0 and 5.8 TB/s.
 
 constexpr int kPutThreads = 256;
 constexpr int kPutTokens = 16, kPutHeads = 2;
