@@ -10,6 +10,9 @@ constexpr int kWorkers = 160;  // CTAs of a call at most: one per SM, B200 has 1
 
 // Requests of up to this many rows (new tokens times query heads of a key head)
 // run the kernel for few rows, others the 256-row tiles of the tensor cores.
+// Measured over 8000 cached tokens, us, few rows / tensor cores: 1 request x 12
+// heads, 40 rows 35.1 / 35.3, 64 rows 39.7 / 35.5; 9 x 3 heads, 40 rows 38.3 /
+// 39.5, 64 rows 44.0 / 40.1; 32 x 8 heads, 40 rows 166 / 206, 64 rows 219 / 207.
 constexpr int kFewRows = 48;
 
 }  // namespace
@@ -25,10 +28,12 @@ cudaError_t launch_cache_attn(const cache::AttnArgs& a, bool f16, int max_q, int
   const long long rows = static_cast<long long>(max_q) * a.G;
   if (rows <= kFewRows)
     return launch_cache_attn_small(a, 0, 0x7fffffff, f16, static_cast<int>(rows), workers, stream);
+  // A batch of one request that may have many rows needs no second kernel for requests with few.
+  const int over = a.R == 1 ? 0 : kFewRows;
   cache::AttnArgs b = a;
   b.ws = static_cast<char*>(a.ws) + cache_attn_small_workspace(kWorkers);
-  cudaError_t e = launch_cache_attn_chunk(b, kFewRows, f16, workers, stream);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = launch_cache_attn_chunk(b, over, f16, workers, stream);
+  if (e != cudaSuccess || over == 0) return e;
   return launch_cache_attn_small(a, 0, kFewRows, f16, kFewRows, workers, stream);
 }
 

@@ -194,17 +194,17 @@ struct Cursor {
     long long rem = u - first;
     h = static_cast<int>(div_small(rem, head));
     rem -= h * head;
-    int tl = 0, th = nt;
+    // the last tile that begins at or before rem: 32 places a step, a lane each
+    const int lane = threadIdx.x & 31;
+    int tl = 0, left = nt;
     long long before = 0;
-    while (th - tl > 1) {
-      const int mid = (tl + th) >> 1;
-      const long long x = S::units_before(a, req, mid);
-      if (x <= rem) {
-        tl = mid;
-        before = x;
-      } else {
-        th = mid;
-      }
+    while (left > 1) {
+      const int step = (left + 31) >> 5, at = lane * step;
+      const long long x = at < left ? S::units_before(a, req, tl + at) : 0;
+      const int hit = 31 - __clz(__ballot_sync(0xffffffffu, at < left && x <= rem));  // lane 0's is
+      before = __shfl_sync(0xffffffffu, x, hit);
+      tl += hit * step;
+      left = min(step, left - hit * step);
     }
     j = tl;
     k = static_cast<int>(rem - before);

@@ -318,6 +318,14 @@ def test_attention(shape, causal, dtype):
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
 
 
+def test_attention_of_fewer_tokens_than_the_bound():
+    """The bound on the new tokens selects the kernel; one request, and several, with far fewer than it says."""
+    for n, kv in (([1], [500]), ([3], [2]), ([1, 30, 0], [500, 40, 7])):
+        b = Batch(n, kv, 6, 2, 32, "bf16")
+        b.ws = vsa.cache_workspace(2000, 6, 2)
+        b.check(*b.run(True, max_q=2000), True)
+
+
 @pytest.mark.parametrize("n,kv,Hq,Hkv,page", [([1], [30011], 2, 1, 256), ([1, 2], [9000, 20000], 8, 2, 16),
                                               ([200], [12345], 2, 1, 64), ([3], [16000], 4, 4, 64),
                                               ([40, 1, 513], [5000, 9000, 4097], 2, 1, 32)])
