@@ -12,8 +12,10 @@
 // in place of 12 and unit sizes of 16 keys were no faster.  What the design does:
 //  - The line of 32-token units (cache_sched.cuh) is cut evenly over the CTAs,
 //    one per SM, and a CTA's share evenly over its warps.  A warp works alone:
-//    its own ring of two units (a bulk copy of 4608 bytes each, or two where a
-//    page ends between), its own softmax state.
+//    its own ring of units (a bulk copy of 4608 bytes each, or two where a page
+//    ends between), its own softmax state.  One more warp fills the rings, a
+//    lane for each: the pages, addresses and bounds of 12 units cost it the
+//    instructions of one.
 //  - Rows are the narrow side of the products: S^T = K Q^T and O^T = V^T P^T
 //    with m16n8k16, 16 keys or channels by 8 rows.  At one row to a key head
 //    that leaves 7/8 of a product unused, and the tensor pipe still idles; the
@@ -62,6 +64,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
   return d;
 }
+__device__ __forceinline__ bool mbar_test_wait(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
@@ -76,6 +89,12 @@ struct PieceMeta {
   int q0, rows;  // the request's first new token, the item's rows
 };
 
+// Where a warp's share of the line begins, for the loads.
+struct Start {
+  int r, h, j, k, nu, nt, total;
+  Request req;
+};
+
 template <int NT, int W, int STAGES>
 struct Smem {
   static constexpr int kRows = 8 * NT;
@@ -83,8 +102,10 @@ struct Smem {
   alignas(16) uint8_t ring[W][STAGES][kUnitBytes];
   alignas(16) uint8_t piece[W][kPieceBytes];  // a warp's first item, begun before its range
   PieceMeta meta[2 * W];                      // [2 w]: that item, [2 w + 1]: one that goes on after its range
-  long long part[W];
-  uint64_t full[W][STAGES];
+  long long part[W + 1];
+  uint64_t full[W][STAGES], empty[W][STAGES];
+  int have[W][STAGES];  // bit i: record i of the unit was loaded, or lies behind the last key
+  Start start[W];
   int abort;
   int join[2][2];  // items this CTA joins: first and last CTA, or -1
 };
@@ -134,7 +155,7 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, const PieceMeta& mt
 }
 
 template <int NT, bool F16, int W, int STAGES>
-__global__ void __launch_bounds__(W * 32, 1)
+__global__ void __launch_bounds__((W + 1) * 32, 1)
     cache_attn_small_kernel(const __grid_constant__ AttnArgs a, const Share share) {
   constexpr int RT = 8 * NT;
   using S = Sched<RT, kUnit, 0>;
@@ -144,8 +165,11 @@ __global__ void __launch_bounds__(W * 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
 
-  if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(&sm.full[warp][s], 1);
+  if (lane == 0 && warp < W) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&sm.full[warp][s], 1);
+      mbar_init(&sm.empty[warp][s], 1);
+    }
     sm.meta[2 * warp].item0 = sm.meta[2 * warp + 1].item0 = -1;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -157,95 +181,131 @@ __global__ void __launch_bounds__(W * 32, 1)
   // the sums over many requests take the place of the warps' pieces until every warp has found its own
   long long* pre = reinterpret_cast<long long*>(&sm.piece[0][0]);
   static_assert(sizeof(sm.piece) >= (kMaxRequests + 1) * 8, "the requests' sums must fit");
-  const Line line = make_line<S, W * 32>(a, share, pre, sm.part);
+  const Line line = make_line<S, (W + 1) * 32>(a, share, pre, sm.part);
   const long long U = line.total;
   if (U == 0) return;
   const long long wanted = (U + W * kMinUnits - 1) / (W * kMinUnits);
   int N = wanted < gridDim.x ? static_cast<int>(wanted) : static_cast<int>(gridDim.x);
   // a batch that does not fill the GPU: whole CTAs for an item, so that items of one length need no joining between CTAs
-  if (N < static_cast<int>(gridDim.x) && line.items > 0 && N > line.items) N -= N % line.items;
+  if (N < static_cast<int>(gridDim.x) && line.items > 0 && line.items <= static_cast<int>(gridDim.x))
+    N = line.items * max(1, N / line.items);
   const int cta = blockIdx.x;
   if (cta >= N) return;
   const Cut cut(U, N);
   const long long cs = cut.start(cta), ce = cut.start(cta + 1);
   const int mine = static_cast<int>(ce - cs);
   const int ws = static_cast<long long>(mine) * warp / W, we = static_cast<long long>(mine) * (warp + 1) / W;
-  const int total = we - ws;
+  const int total = warp < W ? we - ws : 0;
 
   Cursor<S> cc;
   if (total > 0) cc.seek(a, line, cs + ws);
+  if (lane == 0 && warp < W) sm.start[warp] = Start{cc.r, cc.h, cc.j, cc.k, cc.nu, cc.nt, total, cc.req};
   __syncthreads();  // the sums over requests are no longer needed; the flags above are set
 
-  bool ok = true;
-  int issued = 0;
-  if (total > 0) {
-    // ---- loads: a cursor of their own, STAGES units ahead
-    Cursor<S> lc = cc;
-    int lkeys = S::keys(a, lc.req, lc.j);
-    int cache_r = -1, cache_p = 0, my_page = -1;  // 32 entries of the request's row of the table, one a lane
+  if (warp == W) {
+    // ---- loads, lane w for warp w: each lane walks that warp's share and fills the stages it has emptied
+    const bool mine = lane < W && sm.start[lane < W ? lane : 0].total > 0;
+    const Start st = sm.start[mine ? lane : 0];
+    const int w = mine ? lane : 0;
+    Cursor<S> lc;
+    lc.r = st.r, lc.h = st.h, lc.j = st.j, lc.k = st.k, lc.nu = st.nu, lc.nt = st.nt, lc.req = st.req;
+    lc.item0 = 0;
     const int log_rec = a.log_page - 4;  // records of a page
     const uint32_t page_bytes = static_cast<uint32_t>(a.Hkv) * kRecBytes << log_rec;
-    const uint8_t* head_base = a.pages + (static_cast<long long>(lc.h) * kRecBytes << log_rec);
-    uint32_t have_all = 0;  // two bits a stage: record i was loaded, or lies behind the last key
-    // page pi of the request at lc; false: not a page
-    auto find = [&](int pi, const uint8_t*& base) -> bool {
-      if (lc.r != cache_r || static_cast<unsigned>(pi - cache_p) >= 32u) {
-        cache_r = lc.r;
-        cache_p = pi;
-        const int last = (lc.req.kv - 1) >> a.log_page;
-        my_page = pi + lane <= last ? __ldg(a.table + static_cast<long long>(lc.r) * a.max_pages + pi + lane) : -1;
-      }
-      const unsigned page = __shfl_sync(0xffffffffu, my_page, pi - cache_p);
-      if (page >= static_cast<unsigned>(a.num_pages)) {
-        if (lane == 0) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
-        return false;
-      }
-      base = head_base + static_cast<unsigned long long>(page) * page_bytes;
-      return true;
+    int lkeys = 0;
+    const uint8_t* head_base = nullptr;
+    const int32_t* row = nullptr;
+    unsigned page0 = 0, page1 = 0;  // of the next unit's records
+    auto item = [&]() {
+      lkeys = S::keys(a, lc.req, lc.j);
+      head_base = a.pages + (static_cast<long long>(lc.h) * kRecBytes << log_rec);
+      row = a.table + static_cast<long long>(lc.r) * a.max_pages;
     };
-    auto issue = [&](int s) {
-      uint64_t* bar = &sm.full[warp][s];
-      uint8_t* dst = sm.ring[warp][s];
-      uint32_t have = 3;
-      const uint8_t *s0 = nullptr, *s1 = nullptr;
-      if (log_rec > 0) {
-        // both records lie in one page; the second may hold no key, but is there
-        if (lc.k * kUnit < lkeys) {
-          have = find(lc.k * 2 >> log_rec, s0) ? 3 : 0;
-          s0 += (lc.k * 2 & ((1 << log_rec) - 1)) * kRecBytes;
-        } else {
-          have = 4;
-        }
-        if (lane == 0) {
-          if (have == 3) {
-            mbar_arrive_expect_tx(bar, kUnitBytes);
-            bulk_load(dst, s0, kUnitBytes, bar);
-          } else {
-            mbar_arrive(bar);
-          }
-        }
-      } else {
+    auto ask = [&]() {
+      const int rec = lc.k * 2;
+      if (rec * kRecTokens < lkeys) page0 = static_cast<unsigned>(__ldg(row + (rec >> log_rec)));
+      if (log_rec == 0 && (rec + 1) * kRecTokens < lkeys) page1 = static_cast<unsigned>(__ldg(row + rec + 1));
+    };
+    if (mine) {
+      item();
+      ask();
+    }
+    int issued = 0, s = 0, idle = 0;
+    uint32_t parity = 1;
+    uint64_t since = 0;
+    while (true) {
+      const bool want = mine && issued < st.total;
+      if (!__any_sync(0xffffffffu, want)) break;
+      const bool ready = want && mbar_test_wait(smem_u32(&sm.empty[w][s]), parity);
+      if (ready) {
+        uint64_t* bar = &sm.full[w][s];
+        uint8_t* dst = sm.ring[w][s];
         const bool in0 = lc.k * kUnit < lkeys, in1 = lc.k * kUnit + kRecTokens < lkeys;
-        const bool ok0 = in0 && find(lc.k * 2, s0), ok1 = in1 && find(lc.k * 2 + 1, s1);
-        have = (ok0 || !in0 ? 1 : 0) | (ok1 || !in1 ? 2 : 0);
-        if (lane == 0) {
+        const bool ok0 = in0 && page0 < static_cast<unsigned>(a.num_pages);
+        const bool bad0 = in0 && !ok0;
+        const uint8_t* s0 = head_base + static_cast<unsigned long long>(page0) * page_bytes;
+        if (log_rec > 0) {
+          // both records lie in one page; the second may hold no key, but is there
+          sm.have[w][s] = bad0 ? 0 : 3;
+          if (ok0) {
+            mbar_arrive_expect_tx(bar, kUnitBytes);
+            bulk_load(dst, s0 + (lc.k * 2 & ((1 << log_rec) - 1)) * kRecBytes, kUnitBytes, bar);
+          }
+          if (bad0) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
+          if (!ok0) mbar_arrive(bar);
+        } else {
+          const bool ok1 = in1 && page1 < static_cast<unsigned>(a.num_pages);
+          sm.have[w][s] = (bad0 ? 0 : 1) | (in1 && !ok1 ? 0 : 2);
+          if (bad0 || (in1 && !ok1)) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
           if (ok0 || ok1) {
             mbar_arrive_expect_tx(bar, (ok0 ? kRecBytes : 0) + (ok1 ? kRecBytes : 0));
             if (ok0) bulk_load(dst, s0, kRecBytes, bar);
-            if (ok1) bulk_load(dst + kRecBytes, s1, kRecBytes, bar);
+            if (ok1)
+              bulk_load(dst + kRecBytes, head_base + static_cast<unsigned long long>(page1) * page_bytes, kRecBytes, bar);
           } else {
             mbar_arrive(bar);
           }
         }
+        if (++s == STAGES) {
+          s = 0;
+          parity ^= 1;
+        }
+        if (++issued < st.total) {
+          if (++lc.k == lc.nu) {
+            lc.next_item(a, share);
+            item();
+          }
+          ask();
+        }
       }
-      have_all = (have_all & ~(3u << (2 * s))) | ((have & 3) << (2 * s));
-      ++issued;
-      if (issued < total && ++lc.k == lc.nu) {
-        lc.next_item(a, share);
-        lkeys = S::keys(a, lc.req, lc.j);
-        head_base = a.pages + (static_cast<long long>(lc.h) * kRecBytes << log_rec);
+      if (__any_sync(0xffffffffu, ready)) {
+        idle = 0;
+      } else {
+        // bounded like every wait: give up when another warp has, or after 2 s without an emptied stage
+        const uint64_t now = globaltimer_ns();
+        if (idle == 0) since = now;
+        idle = 1;
+        if (*static_cast<volatile int*>(&sm.abort) || now - since > kTimeoutNs) {
+          if (lane == 0) {
+            sm.abort = 1;
+            atomicCAS(a.status, 0u, (unsigned)VSA_ERR_TIMEOUT);
+          }
+          // every copy issued must land before the CTA's shared memory is released
+          for (int x = 0; x < STAGES; ++x)
+            if (mine && issued > x) {
+              const int last = issued - 1 - ((issued - 1 - x) % STAGES);
+              mbar_wait_drain(&sm.full[w][x], (last / STAGES) & 1, kTimeoutNs);
+            }
+          break;
+        }
+        __nanosleep(40);
       }
-    };
+    }
+    __syncwarp();
+  }
+
+  bool ok = true;
+  if (total > 0) {
     uint32_t qf[NT][16];
     float rs[NT][2], m[NT][2], l[NT][2], base[NT][2];  // base: -m, or 0 where there is none yet
     int lim[NT][2];
@@ -273,8 +333,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
       }
     };
-    load_q();  // on its way while the first records are found
-    for (int i = 0; i < STAGES && i < total; ++i) issue(i);
+    load_q();
 
     for (int i = 0; i < total; ++i) {
       if (i == 0 || cc.k == 0) {
@@ -319,7 +378,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         ok = false;
         break;
       }
-      const uint32_t have = have_all >> (2 * s) & 3;
+      const uint32_t have = sm.have[warp][s];
       const int key0 = cc.k * kUnit;
       if (key0 < seen) {
         const uint8_t* unit = sm.ring[warp][s];
@@ -450,7 +509,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
       }
       __syncwarp();  // the unit has been read
-      if (issued < total) issue(s);
+      if (lane == 0) mbar_arrive(&sm.empty[warp][s]);
       if (++s == STAGES) {
         s = 0;
         parity ^= 1;
@@ -502,14 +561,6 @@ __global__ void __launch_bounds__(W * 32, 1)
         ++cc.k;
       }
     }
-    if (!ok) {
-      // a wait ran out: every copy issued must land before the CTA's shared memory is released
-      for (int s = 0; s < STAGES; ++s)
-        if (issued > s) {
-          const int last = issued - 1 - ((issued - 1 - s) % STAGES);
-          mbar_wait_drain(&sm.full[warp][s], (last / STAGES) & 1, kTimeoutNs);
-        }
-    }
   }
   __syncthreads();
   if (sm.abort) return;
@@ -537,7 +588,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     const bool whole = mt.item0 >= cs && mt.item0 + mt.nu <= ce;
     const int slot = mt.item0 < cs ? 0 : 1;
     if (!whole) cross[slot] = mt;
-    for (int row = warp; row < mt.rows; row += W) {
+    for (int row = warp; row < mt.rows; row += W + 1) {
       const bool in = group >> lane & 1;
       RowPart t = join_weights(in ? mine_at[RT * 128 + row] : -INFINITY, in ? mine_at[RT * 129 + row] : 0.0f);
       for (unsigned left = group; left; left &= left - 1) {
@@ -578,7 +629,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     const int first = sm.join[x][0], last = sm.join[x][1];
     if (first < 0) continue;
     const PieceMeta mt = cross[x];
-    for (int row = warp; row < mt.rows; row += W) {
+    for (int row = warp; row < mt.rows; row += W + 1) {
       auto part_of = [&](int w) { return parts + (static_cast<size_t>(w) * 2 + (w == first ? 1 : 0)) * kPart; };
       RowPart t;
       t.m = -INFINITY;
@@ -615,7 +666,7 @@ cudaError_t launch_small(const AttnArgs& a, const Share& share, bool f16, int nu
   static SmemAllowed allowed[2];  // fp16, bf16
   cudaError_t e = allowed[f16 ? 0 : 1].ensure(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  kern<<<num_sms < kMaxWorkers ? num_sms : kMaxWorkers, W * 32, smem, stream>>>(a, share);
+  kern<<<num_sms < kMaxWorkers ? num_sms : kMaxWorkers, (W + 1) * 32, smem, stream>>>(a, share);
   return cudaGetLastError();
 }
 
@@ -628,8 +679,8 @@ size_t cache_attn_small_workspace(int num_workers) {
 cudaError_t launch_cache_attn_small(const cache::AttnArgs& a, int over, int upto, bool f16, int rows, int num_sms,
                                     cudaStream_t stream) {
   const Share share{over, upto};
-  return rows <= 8 ? launch_small<1, 12, 3>(a, share, f16, num_sms, stream)
-                   : launch_small<2, 8, 4>(a, share, f16, num_sms, stream);
+  return rows <= 8 ? launch_small<1, 15, 2>(a, share, f16, num_sms, stream)
+                   : launch_small<2, 7, 4>(a, share, f16, num_sms, stream);
 }
 
 }  // namespace vsa
