@@ -11,9 +11,10 @@ constexpr int kWorkers = 160;  // CTAs of a call at most: one per SM, B200 has 1
 // Requests of up to this many rows (new tokens times query heads of a key head)
 // run the kernel for few rows, others the 256-row tiles of the tensor cores.
 // Measured over 8000 cached tokens, us, few rows / tensor cores: 1 request x 12
-// heads, 40 rows 35.1 / 35.3, 64 rows 39.7 / 35.5; 9 x 3 heads, 40 rows 38.3 /
-// 39.5, 64 rows 44.0 / 40.1; 32 x 8 heads, 40 rows 166 / 206, 64 rows 219 / 207.
-constexpr int kFewRows = 48;
+// heads, 40 rows 30.3 / 32.6, 64 rows 34.1 / 32.7; 9 requests of up to 64 rows x
+// 3 heads 38.7 / 57.0, 32 x 8 heads 200 / 210 (some of their requests have fewer
+// rows, so that with a lower border both kernels run).
+constexpr int kFewRows = 64;
 
 }  // namespace
 

@@ -25,7 +25,7 @@
 // Bound: the rows' threads (a tile's softmax, then the products that wait for
 // it), as in the fine stage; the conversion (256 values a key and CTA, whatever
 // its rows) runs beside it and waits a quarter of its time.  6240 tokens over
-// 32760, 12 heads: 1.33 ms, 940 TFLOP/s of 16-bit products where the fine stage
+// 32760, 12 heads: 1.29 to 1.35 ms, 930 to 970 TFLOP/s of 16-bit products where the fine stage
 // does 970 to 990.  Every fourth exponential by a polynomial was 7% slower: the
 // issue slots, not ex2, are what the rows' threads share with the conversion.
 //
@@ -48,7 +48,7 @@ constexpr int kThreads = 512;
 constexpr int kRowTile = 256, kKeyTile = 128;
 constexpr int kStagesK = 3, kStagesV = 2, kSegs = 4;
 // An item's rows of Q, first product and output take a CTA some 6 to 9 us, a unit 2.4 us (4 x 1023 on 5000: 157 us with
-// 4, 162 with 3, 170 with 2, 196 with 0; one long item does not care).
+// 4, 162 with 3, 170 with 2, 196 with 0, a pass; one long item does not care).
 constexpr int kItemCost = 4;
 constexpr uint32_t kHalfBytes = 128 * 128;       // 128 rows x 64 fp16 (one 128-B swizzle column)
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // 128 rows x 128 fp16

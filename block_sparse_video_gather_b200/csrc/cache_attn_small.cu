@@ -3,13 +3,12 @@
 //
 // Bound: HBM on paper, the issue slots beside it.  A cached token and head are
 // 144 bytes, 0.022 ns at 6561 GB/s; the work beside the loads is to make 256
-// fp16 values of them, some 300 warp instructions per 16 tokens, which at the
-// issue rate reached (0.5 per scheduler and cycle) take 43 us where the loads
-// take 38 for 126360 tokens x 12 heads: 57 us in all, 3.8 TB/s, of which about
-// 14 are the launch, finding the place, the first loads and the joins (a copy
-// that only loads takes 46).  A single token over 777 is 10.5 us, nearly all of
-// it those.  Overlapping a unit's values with the next one's scores, 16 warps
-// in place of 12 and unit sizes of 16 keys were no faster.  What the design does:
+// fp16 values of them, some 290 warp instructions per 16 tokens.  126360 tokens
+// x 12 heads: 50 us, 4.3 TB/s; a copy that only loads took 46 of the 57 us before
+// the loads had a warp of their own, about 10 of them the launch, finding the
+// place, the first loads and the joins.  A single token over 777 is 10 us, nearly
+// all of it those.  Adding a unit's values beside the next one's scores and units
+// of 16 tokens were no faster.  What the design does:
 //  - The line of 32-token units (cache_sched.cuh) is cut evenly over the CTAs,
 //    one per SM, and a CTA's share evenly over its warps.  A warp works alone:
 //    its own ring of units (a bulk copy of 4608 bytes each, or two where a page
