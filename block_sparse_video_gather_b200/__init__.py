@@ -939,20 +939,20 @@ class KVCache:
             raise ValueError("reserve comes before append")
         cache_append(k, v, self.slots, self.pages)
 
-    def attend(self, q, causal: bool = True, cu=None, o_out=None, lse_out=None):
+    def attend(self, q, causal: bool = True, cu=None, o_out=None, lse_out=None, max_q: int | None = None):
         """q [tokens, Hq, 128], rows cu[r] .. cu[r+1] of request r (default: those of the last reserve), over the
-        cache -> (o, lse [tokens, Hq])."""
-        return cache_attn(q, self.cu if cu is None else cu, self.kv_len, self.table, self.pages, self.max_q,
+        cache -> (o, lse [tokens, Hq]).  max_q: the most rows of a request in this call (default: the cache's)."""
+        return cache_attn(q, self.cu if cu is None else cu, self.kv_len, self.table, self.pages, max_q or self.max_q,
                           self.workspace, causal, o_out, lse_out)
 
     def attend_chunk(self, q):
         """q [R,S,Hq,128], the queries of each request's next chunk, over all its cached tokens -> (o [R,S,Hq,128],
-        lse [R,S,Hq])."""
+        lse [R,S,Hq]).  S is at most the cache's max_q."""
         R, S, H, D = q.shape
-        if R != self.R:
-            raise ValueError(f"q holds {R} requests, the cache {self.R}")
+        if R != self.R or S > self.max_q:
+            raise ValueError(f"q holds {R} requests of {S} rows, the cache {self.R} of at most max_q = {self.max_q}")
         cu = _torch().arange(0, (R + 1) * S, S, dtype=_torch().int32, device=q.device) if S else self.cu * 0
-        o, lse = self.attend(q.view(R * S, H, D), causal=False, cu=cu)
+        o, lse = self.attend(q.view(R * S, H, D), causal=False, cu=cu, max_q=max(S, 1))
         return o.view(R, S, H, D), lse.view(R, S, H)
 
     def release(self, drop):

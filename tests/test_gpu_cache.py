@@ -605,6 +605,8 @@ def test_chunks_of_a_video(dtype):
                 assert np.all(np.abs(f64(o[b, :, h]) - eo) <= to)
                 assert np.all(np.abs(f64(lse[b, :, h]) - el) <= 2 * tl)
             past[b] = [np.concatenate([past[b][0], rk[b]]), np.concatenate([past[b][1], rv[b]])]
+    with pytest.raises(ValueError, match="max_q"):
+        vsa.KVCache(num_pages=4, Hq=H, max_requests=B).attend_chunk(q)
     with pytest.raises(ValueError, match="past"):
         vsa.Forward(plan, B, H, 2, gated=True, dtype=TDT[dtype])(q, k, v, gate=q, past=cache.attend_chunk(q))
 
