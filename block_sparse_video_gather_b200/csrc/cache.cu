@@ -22,12 +22,14 @@ using namespace cache;
 // itself in shared memory -- R <= 4096 lengths are 32 KB out of L2 -- and then
 // fills its share of the slots and of the new table entries, finding the
 // request by bisection; so the call is one launch with nothing to wait for.
-// The bound is latency: the largest call writes some MB.  8 requests 4.6 us, 4096
-// requests with 1.02 M new tokens 14 us, of which the slots take 7 (four CTAs'
+// The bound is latency: the largest call writes some MB.  8 requests 4.4 us, 4096
+// requests with 1.02 M new tokens 11.8 us, of which the slots take half (four CTAs'
 // worth of passes side by side, or eight tokens a thread, were slower).
 
-constexpr int kTabThreads = 512;
-constexpr int kTabSlots = kTabThreads * 4;  // slots of one pass of a CTA
+// Threads of a CTA: with many requests the sums and look-ups of a thread are a
+// chain, and twice the threads shorten it (4096 requests 11.8 us, 13.9 with 512);
+// with few, more threads only cost (8 requests 4.4 us, 5.4 with 1024).
+constexpr int kTabThreads = 512, kTabThreadsMany = 1024;
 
 // Inclusive sum over the threads of a CTA of one value each.
 __device__ __forceinline__ long long block_scan(long long v, long long* part) {
@@ -40,9 +42,14 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part) {
   __syncthreads();  // part may still be read from the scan before
   if (lane == 31) part[warp] = v;
   __syncthreads();
-  long long before = 0;
-  for (int w = 0; w < warp; ++w) before += part[w];
-  return v + before;
+  long long p = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, p, d);
+    if (lane >= d) p += u;
+  }
+  const long long before = __shfl_sync(0xffffffffu, p, warp > 0 ? warp - 1 : 0);
+  return v + (warp > 0 ? before : 0);
 }
 
 // Place of entry i of an array in shared memory: with 8 entries a thread (4096
@@ -60,16 +67,17 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_constant__ CacheTablesArgs a) {
+__global__ void __launch_bounds__(kTabThreadsMany) cache_tables_kernel(const __grid_constant__ CacheTablesArgs a) {
   extern __shared__ int tab_smem[];
-  __shared__ long long part[kTabThreads / 32];
+  __shared__ long long part[kTabThreadsMany / 32];
   __shared__ int s_pages;
   int* tok = tab_smem;            // [R + 1] first new token
   const int words = spread(a.R) + 1;
   int* pag = tok + words;         // [R + 1] first new page, from free_start
   int* len = pag + words;         // [R] cached tokens; -1: refused
   int* fresh = len + words;       // [R] new tokens, then new pages
-  const int per = (a.R + kTabThreads - 1) / kTabThreads;
+  const int threads = blockDim.x;
+  const int per = (a.R + threads - 1) / threads;
   const int r0 = min(static_cast<int>(threadIdx.x) * per, a.R), r1 = min(r0 + per, a.R);
   const int P = 1 << a.log_page;
   const long long cap = static_cast<long long>(a.max_pages) << a.log_page;
@@ -78,7 +86,7 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
   if (threadIdx.x == 0) s_pages = 0;
 
   // lengths come in whole lines, then each thread looks after `per` requests
-  for (int r = threadIdx.x; r < a.R; r += kTabThreads) {
+  for (int r = threadIdx.x; r < a.R; r += threads) {
     len[spread(r)] = __ldg(a.kv_len + r);
     fresh[spread(r)] = __ldg(a.new_len + r);
   }
@@ -127,12 +135,12 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
   __syncthreads();
   const int pages = s_pages, tokens = tok[spread(a.R)];
   if (lead) {
-    for (int r = threadIdx.x; r <= a.R; r += kTabThreads) a.cu[r] = tok[spread(r)];
+    for (int r = threadIdx.x; r <= a.R; r += threads) a.cu[r] = tok[spread(r)];
     if (threadIdx.x == 0) *a.free_next = start + pages;
   }
 
   // entries of the pages taken: page i of a request's new ones follows those it has
-  for (int e = blockIdx.x * kTabThreads + threadIdx.x; e < pages; e += gridDim.x * kTabThreads) {
+  for (int e = blockIdx.x * threads + threadIdx.x; e < pages; e += gridDim.x * threads) {
     const int r = last_at_most(pag, a.R, e);
     const int had = (len[spread(r)] + P - 1) >> a.log_page;
     a.table[static_cast<long long>(r) * a.max_pages + had + (e - pag[spread(r)])] = __ldg(a.free_pages + start + e);
@@ -140,15 +148,15 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const __grid_
 
   // slots; a token of a page taken now reads its id from the stack, not from the entry above
   const int page_limit = 0x7fffffff >> a.log_page;
-  for (long long i0 = static_cast<long long>(blockIdx.x) * kTabSlots + threadIdx.x * 4; i0 < a.max_tokens;
-       i0 += static_cast<long long>(gridDim.x) * kTabSlots) {
+  for (long long i0 = static_cast<long long>(blockIdx.x) * threads * 4 + threadIdx.x * 4; i0 < a.max_tokens;
+       i0 += static_cast<long long>(gridDim.x) * threads * 4) {
     int4 out = make_int4(-1, -1, -1, -1);
     int* ov = &out.x;
     int r = i0 < tokens ? last_at_most(tok, a.R, static_cast<int>(i0)) : 0;
     int known_r = -1, known_pi = -1, page = -1;  // neighbours are mostly in one page
     for (int j = 0; j < 4; ++j) {
+      if (i0 + j >= tokens) break;
       const int i = static_cast<int>(i0) + j;
-      if (i >= tokens) break;
       while (tok[spread(r + 1)] <= i) ++r;  // ends: tok[R] = tokens > i
       const int kv = len[spread(r)];
       if (kv < 0) continue;
@@ -391,7 +399,8 @@ long long put_grid(int T, int Hkv) {
 }  // namespace
 
 cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStream_t stream) {
-  const long long passes = (static_cast<long long>(a.max_tokens) + kTabSlots - 1) / kTabSlots;
+  const int threads = a.R > kTabThreads ? kTabThreadsMany : kTabThreads;
+  const long long passes = (static_cast<long long>(a.max_tokens) + 4 * threads - 1) / (4 * threads);
   const int grid = static_cast<int>(passes < 1 ? 1 : passes < num_sms ? passes : num_sms);
   const int smem = 4 * (spread(a.R) + 1) * 4;
   if (smem > 40 * 1024) {  // more than the default limit only for R > 2275
@@ -399,7 +408,7 @@ cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStrea
                                          4 * (spread(kMaxRequests) + 1) * 4);
     if (e != cudaSuccess) return e;
   }
-  cache_tables_kernel<<<grid, kTabThreads, smem, stream>>>(a);
+  cache_tables_kernel<<<grid, threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 

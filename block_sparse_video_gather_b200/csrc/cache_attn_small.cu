@@ -13,8 +13,8 @@
 //    one per SM, and a CTA's share evenly over its warps.  A warp works alone:
 //    its own ring of units (a bulk copy of 4608 bytes each, or two where a page
 //    ends between), its own softmax state.  One more warp fills the rings, a
-//    lane for each: the pages, addresses and bounds of 12 units cost it the
-//    instructions of one.
+//    lane for each: pages, addresses and bounds of as many units as there are
+//    warps cost it the instructions of one.
 //  - Rows are the narrow side of the products: S^T = K Q^T and O^T = V^T P^T
 //    with m16n8k16, 16 keys or channels by 8 rows.  At one row to a key head
 //    that leaves 7/8 of a product unused, and the tensor pipe still idles; the
