@@ -50,6 +50,10 @@ constexpr int kStagesK = 3, kStagesV = 2, kSegs = 4;
 // An item's rows of Q, first product and output take a CTA some 6 to 9 us, a unit 2.4 us (4 x 1023 on 5000: 157 us with
 // 4, 162 with 3, 170 with 2, 196 with 0, a pass; one long item does not care).
 constexpr int kItemCost = 4;
+// Places of the line that a CTA gets at least.  Shorter shares end sooner but have more parts to join: 3 requests of
+// 78 rows on 1483, 8 heads, 58.2 us with 8, 50.8 with 4, 45.3 with 2; one of 61 x 3 rows on 19525 32.3 with 4, 34.5
+// with 2 (27.3 now, with the join spread wider).
+constexpr int kMinPlaces = 3;
 constexpr uint32_t kHalfBytes = 128 * 128;       // 128 rows x 64 fp16 (one 128-B swizzle column)
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // 128 rows x 128 fp16
 constexpr uint32_t kSmemQ = 0;
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sV = smem + kSmemV;
   Barriers* bars = reinterpret_cast<Barriers*>(smem + kSmemBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x, N = gridDim.x;
+  const int cta = blockIdx.x;
 
   // the sums over many requests use the K ring before anything else does
   const Line line = make_line<S, kThreads>(a, share, reinterpret_cast<long long*>(sK),
@@ -187,9 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long U = line.total;
   Joint* joint = static_cast<Joint*>(a.ws) + cta;
   if (threadIdx.x == 0) joint->last = -1;
+  const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), (U + kMinPlaces - 1) / kMinPlaces));
+  if (cta >= N) return;  // N = 0: no request for this kernel
   const Cut cut(U, N);
   const long long cs = cut.start(cta), ce = cut.start(cta + 1);
-  if (cs == ce) return;
   Cursor<S> cur;
   if (warp == 1) cur.seek(a, line, cs);
   __syncthreads();
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();  // read before the next item's Q takes the rows
         } else {
           // four channels of 256 rows after another: the threads of a warp store 512 bytes in a row
-          float* part = parts_of(a.ws, N) + (static_cast<size_t>(cta) * 2 + (cur.k0 > 0 ? 0 : 1)) * part_floats<kRowTile>();
+          float* part = parts_of(a.ws, gridDim.x) + (static_cast<size_t>(cta) * 2 + (cur.k0 > 0 ? 0 : 1)) * part_floats<kRowTile>();
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t ov[32];
@@ -708,51 +713,115 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the rows of the items that more than one CTA worked on.  A CTA takes 32
-// rows, a lane a row, a warp 16 of its channels: reads of 512 bytes in a row.
+// rows, a lane a row (reads of 512 bytes in a row).  Up to 8 parts, as of long
+// batches, a warp takes 16 channels and goes through the parts; more, as of one
+// item over many CTAs (148 parts one after another took 70 us), a warp takes
+// every eighth part, and the warps' sums are joined; the next three CTAs, which
+// have no item of their own then, take 32 channels each, as the first does.
 constexpr int kJoinRows = 32, kJoinWarps = 8;
+struct RowSum {
+  float m, l;
+};
+// Scales of what is there and of a part under their joint maximum; without a
+// maximum a part has nothing but zeros, or the NaN of its scores.
+__device__ __forceinline__ void join_scales(RowSum& t, float pm, float pl, float& w0, float& w1) {
+  const float mn = fmaxf(t.m, pm);
+  w0 = t.m == -INFINITY ? 1.0f : ex2_approx(t.m - mn);
+  w1 = pm == -INFINITY ? 1.0f : ex2_approx(pm - mn);
+  t.l = w0 * t.l + w1 * pl;
+  t.m = mn;
+}
+__device__ __forceinline__ float4 scaled_sum(float w0, float4 a, float w1, float4 b) {
+  return make_float4(w0 * a.x + w1 * b.x, w0 * a.y + w1 * b.y, w0 * a.z + w1 * b.z, w0 * a.w + w1 * b.w);
+}
+
 template <bool F16>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     cache_attn_join_kernel(const __grid_constant__ AttnArgs a, int workers) {
-  const int first = blockIdx.x, warp = threadIdx.x >> 5;
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x & 31);
-  const Joint jt = static_cast<const Joint*>(a.ws)[first];
-  if (jt.last < 0 || row >= jt.rows) return;
+  __shared__ float4 sums[kJoinWarps][8][kJoinRows];
+  __shared__ RowSum row_sums[kJoinWarps][kJoinRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinRows + lane;
+  const Joint* joints = static_cast<const Joint*>(a.ws);
+  int first = blockIdx.x, quarter = 0;
+  if (joints[first].last < 0) {
+    for (int k = 1; k < 4 && k <= first && quarter == 0; ++k)
+      if (joints[first - k].last - (first - k) >= 8) quarter = k;
+    if (quarter == 0) return;
+    first -= quarter;
+  }
+  const Joint jt = joints[first];
+  if (static_cast<int>(blockIdx.y) * kJoinRows >= jt.rows) return;  // the whole CTA
+  const bool real = row < jt.rows;
   constexpr size_t kPart = part_floats<kRowTile>();
   const float* parts = parts_of(a.ws, workers);
-  float m = -INFINITY, l = 0.0f;
-  float o[16];
-#pragma unroll
-  for (int x = 0; x < 16; ++x) o[x] = 0.0f;
-#pragma unroll 2
-  for (int w = first; w <= jt.last; ++w) {
-    const float* f = parts + (static_cast<size_t>(w) * 2 + (w == first ? 1 : 0)) * kPart;
-    float4 p[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) p[x] = reinterpret_cast<const float4*>(f)[(warp * 4 + x) * kRowTile + row];
-    const float pm = f[kRowTile * 128 + row], pl = f[kRowTile * 129 + row];
-    const float mn = fmaxf(m, pm);
-    // without a maximum a part has nothing but zeros, or the NaN of its scores
-    const float w0 = m == -INFINITY ? 1.0f : ex2_approx(m - mn), w1 = pm == -INFINITY ? 1.0f : ex2_approx(pm - mn);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      o[4 * x] = w0 * o[4 * x] + w1 * p[x].x;
-      o[4 * x + 1] = w0 * o[4 * x + 1] + w1 * p[x].y;
-      o[4 * x + 2] = w0 * o[4 * x + 2] + w1 * p[x].z;
-      o[4 * x + 3] = w0 * o[4 * x + 3] + w1 * p[x].w;
-    }
-    l = w0 * l + w1 * pl;
-    m = mn;
-  }
+  auto part = [&](int w) { return parts + (static_cast<size_t>(w) * 2 + (w == first ? 1 : 0)) * kPart; };
   const int rr = jt.j * kRowTile + row, token = rr / a.G;
   const long long dst = (static_cast<long long>(jt.q0) + token) * a.Hq + jt.h * a.G + (rr - token * a.G);
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-  uint32_t w[8];
+  RowSum t{-INFINITY, 0.0f};
+  if (jt.last - first < 8) {
+    float4 o[4];
 #pragma unroll
-  for (int x = 0; x < 8; ++x) w[x] = pack_half2<F16>(o[2 * x] * inv, o[2 * x + 1] * inv);
-  uint4* out = reinterpret_cast<uint4*>(a.o + dst * 128 + warp * 16);
-  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (warp == 0) a.lse[dst] = l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int x = 0; x < 4; ++x) o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!real) return;
+#pragma unroll 2
+    for (int w = first; w <= jt.last; ++w) {
+      const float* f = part(w);
+      float4 p[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) p[x] = reinterpret_cast<const float4*>(f)[(warp * 4 + x) * kRowTile + row];
+      float w0, w1;
+      join_scales(t, f[kRowTile * 128 + row], f[kRowTile * 129 + row], w0, w1);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = scaled_sum(w0, o[x], w1, p[x]);
+    }
+    const float inv = t.l != 0.0f ? 1.0f / t.l : 0.0f;
+    uint32_t w[8];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      w[2 * x] = pack_half2<F16>(o[x].x * inv, o[x].y * inv);
+      w[2 * x + 1] = pack_half2<F16>(o[x].z * inv, o[x].w * inv);
+    }
+    uint4* out = reinterpret_cast<uint4*>(a.o + dst * 128 + warp * 16);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    const int group0 = quarter * 8;  // groups of 4 channels
+    float4 s[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) s[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (real) {
+#pragma unroll 2
+      for (int w = first + warp; w <= jt.last; w += kJoinWarps) {
+        const float* f = part(w);
+        float4 p[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) p[x] = reinterpret_cast<const float4*>(f)[(group0 + x) * kRowTile + row];
+        float w0, w1;
+        join_scales(t, f[kRowTile * 128 + row], f[kRowTile * 129 + row], w0, w1);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s[x] = scaled_sum(w0, s[x], w1, p[x]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sums[warp][x][lane] = s[x];
+    row_sums[warp][lane] = t;
+    __syncthreads();
+    t = RowSum{-INFINITY, 0.0f};
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+      float w0, w1;
+      join_scales(t, row_sums[i][lane].m, row_sums[i][lane].l, w0, w1);
+      o = scaled_sum(w0, o, w1, sums[i][warp][lane]);
+    }
+    const float inv = t.l != 0.0f ? 1.0f / t.l : 0.0f;
+    uint2 w;
+    w.x = pack_half2<F16>(o.x * inv, o.y * inv);
+    w.y = pack_half2<F16>(o.z * inv, o.w * inv);
+    if (real) reinterpret_cast<uint2*>(a.o + dst * 128)[group0 + warp] = w;
+  }
+  if (real && warp == 0 && quarter == 0) a.lse[dst] = t.l != 0.0f ? (t.m + __log2f(t.l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
