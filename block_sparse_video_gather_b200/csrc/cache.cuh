@@ -30,6 +30,13 @@ constexpr int kRecTokens = 16;
 constexpr int kRecBytes = 2304;
 constexpr int kRecV = 1024, kRecKS = 2048, kRecVS = 2176;
 constexpr int kMaxRequests = 4096;
+// Softmax numerators are fp16 on their way into P V, and 2^8 at most against the
+// maximum in use, which moves only when a score exceeds it by 8 (log2).  Taken
+// against that maximum less kLift, with which the parts of a row and its lse are
+// kept too, they reach 2^15, and what fp16 drops at its lower end is 2^-32 of the
+// largest instead of 2^-25: over 126360 tokens a tail there can weigh 4e-3 of a
+// row, and only P V would lose it, not the denominator.
+constexpr float kLift = 7.0f;
 
 // Eight fp32 values -> eight E2M1 codes in one word; value 0 in the low nibble
 // of byte 0.  Round to nearest, ties to even, saturate at +-6.

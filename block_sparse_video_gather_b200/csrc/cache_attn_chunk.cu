@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return static_cast<unsigned>(__ldg(a.table + static_cast<long long>(cur.r) * a.max_pages + (rec >> log_rec)));
       };
       unsigned page = page_at(0);
-      float m_used = -INFINITY, l = 0.0f;
+      float m_used = -INFINITY, l = 0.0f;  // m_used: a maximum less kLift
       for (int t = 0; t < n && active; ++t) {
         const int key0 = (cur.k0 + t) * kKeyTile;
         const unsigned bad_recs = __ballot_sync(0xffffffffu, page >= static_cast<unsigned>(a.num_pages));
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               a1 = max3f(a1, __uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3]));
             }
             const float mt = fmaxf(a0, a1) * sl2;
-            if (mt > -INFINITY) m_used = mt;
+            if (mt > -INFINITY) m_used = mt - kLift;
             if (__any_sync(0xffffffffu, mt > -INFINITY)) continue;
           }
 #pragma unroll
@@ -614,12 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           f2unpack(acc[1], s2, s3);
           part = (s0 + s1) + (s2 + s3);
           const float mt = fmaxf(a0, a1) * sl2;
-          const bool grow = mt > m_used + 8.0f;
+          const bool grow = mt > m_used + (8.0f + kLift);
           if (!__any_sync(0xffffffffu, grow)) break;
           if (grow) {
             rescale = t > 0 && m_used != -INFINITY;
-            alpha = rescale ? ex2_approx(m_used - mt) : 1.0f;
-            m_used = mt;
+            alpha = rescale ? ex2_approx(m_used - (mt - kLift)) : 1.0f;
+            m_used = mt - kLift;
           }
         }
         l = l * alpha + part;

@@ -31,7 +31,8 @@
 //    largest).  Only the numerators are rounded, to fp16.
 //  - Online softmax in the log2 domain; the maximum moves (and the output is
 //    rescaled) only when a score exceeds it by 8, so one vote per unit takes
-//    the place of the reduction.
+//    the place of the reduction.  Numerators are taken against the maximum less
+//    kLift (cache.cuh).
 // Sums, maxima and denominators are fp32.  Parts are joined in a fixed order:
 // the result does not depend on which CTA comes last.
 #include <cuda_fp16.h>
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
   bool ok = true;
   if (total > 0) {
     uint32_t qf[NT][16];
-    float rs[NT][2], m[NT][2], l[NT][2], base[NT][2];  // base: -m, or 0 where there is none yet
+    float rs[NT][2], m[NT][2], l[NT][2], base[NT][2];  // m: the maximum less kLift; base: -m, or 0 where there is none yet
     int lim[NT][2];
     float acc[NT][8][4];
     int lim_min = 0, seen = 0;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float t = fmaxf(max3f(sc[n][0][e], sc[n][0][e + 2], sc[n][1][e]), sc[n][1][e + 2]) * rs[n][e];
-            grow |= t > m[n][e] + 8.0f;
+            grow |= t > m[n][e] + (8.0f + kLift);
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-              if (t > m[n][e] + 8.0f) {
+              if (t > m[n][e] + (8.0f + kLift)) {
+                t -= kLift;
                 const float alpha = ex2_approx(m[n][e] - t);  // 0 for the first maximum
                 m[n][e] = t;
                 base[n][e] = -t;

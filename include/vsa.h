@@ -538,7 +538,8 @@ VSA_API int vsa_cache_read_nvfp4(vsa_dtype_t dtype, const int32_t *slots, int T,
  *              graphs that do not overlap may share one).
  * The codes' values, q (bf16: times a power of two per row) and the softmax
  * numerators enter the products as fp16, which holds all but the numerators
- * exactly; sums are fp32.
+ * exactly: those to 2^-11 of themselves, and below 2^-21 of the row's largest
+ * (as the worker that takes the key has seen it) to 2^-32 of that; sums are fp32.
  * Device-side checks, each setting VSA_ERR_BAD_INDEX: positions in pages
  * outside [0, num_pages) are left out; kv_len is cut to [0, max_pages *
  * page_tokens], cu to ascending values within [0, T].

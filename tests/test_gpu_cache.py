@@ -3,6 +3,8 @@
 Block tables and slots, codes and scales are whole numbers and compared exactly; attention and the merge within the
 bounds derived at cache_forms.tolerances and below.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -670,3 +672,74 @@ def test_steps_of_a_serving_loop():
     eager([33, 1, 2], rand(36, Hq), rand(36, Hkv), rand(36, Hkv))
     pages = np.concatenate([cache.table[r, :-(-kept[r].shape[1] // 16)].cpu().numpy() for r in range(R)])
     assert len(set(pages.tolist())) == len(pages)
+
+
+# ---------------------------------------------------------------------------
+# One dominant key before a long tail
+# ---------------------------------------------------------------------------
+
+
+def _attend_shared(q, kv, page, pages, table, ws_q):
+    """Requests of the rows of q [R, n, Hq, 128] over the same cached tokens."""
+    R, n, Hq = q.shape[:3]
+    ws = vsa.cache_workspace(ws_q, Hq, pages.shape[1])
+    return vsa.cache_attn(q.reshape(R * n, Hq, 128), i32(np.arange(R + 1) * n), i32([kv] * R), table, pages, ws_q, ws,
+                          causal=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("where", [0, 1500, 29999])
+@pytest.mark.parametrize("R,n,Hq", [(2368, 1, 1), (1184, 1, 16), (1, 256, 148)],
+                         ids=["one row", "16 rows", "256-row tiles"])
+def test_attention_of_a_dominant_key_and_its_tail(R, n, Hq, where, dtype):
+    """One key of score 17.5 and value 0, all others of score 0 and value 6: each weighs 2^-25.2 of the first, together
+    they are the whole output.  As many items as warps (or CTAs), so that the workers that hold the dominant key hold
+    most of an item's tail too.
+
+    A numerator is off by 2^-11 of itself, or by 2^-32 of the largest where fp16 holds it as a subnormal (the largest
+    is between 2^7 and 2^15, the subnormal half step 2^-25); the other terms are those of cache_forms.tolerances."""
+    L, page = 30000, 64
+    k = torch.zeros((L, 1, 128), dtype=TDT[dtype])
+    v = torch.full((L, 1, 128), 6.0, dtype=TDT[dtype])
+    k[where, 0, 0], v[where] = 6.0, 0.0
+    n_pages = -(-L // page)
+    pages = vsa.cache_pages(n_pages, 1, page)
+    vsa.cache_append(k.cuda(), v.cuda(), i32(np.arange(L)), pages)
+    table = i32(np.tile(np.arange(n_pages), (R, 1)))
+    q = torch.zeros((R, n, Hq, 128), dtype=TDT[dtype], device="cuda")
+    q[..., 0] = 33.0
+    o, lse = _attend_shared(q, L, page, pages, table, n)
+    eo, el, spread, reach = F.attention(f64(q[0, 0, :1]), f64(k[:, 0]), f64(v[:, 0]), [L])
+    assert 2.0**-26 < math.exp(-33 * 6 / math.sqrt(128)) < 2.0**-25
+    score = 2.0**-17 * reach[0] + 2.0**-22 * (1 + abs(el[0]))
+    sums = L * 2.0**-24 + 2.0**-20
+    to = (2.0**-11 + 2 * score + 2 * sums) * spread[0] + L * 2.0**-32 * 6
+    to = to + (2.0**-8 if dtype == "bf16" else 2.0**-11) * (eo[0] + to) + 2.0**-25
+    assert np.all(to < eo[0] / 20)  # a lost tail would show
+    err = (o.double() - torch.from_numpy(eo[0]).cuda()).abs().amax((0, 1)).cpu().numpy()
+    assert np.all(err <= to), (err.max(), to.max(), eo[0].max())
+    assert float((lse.double() - el[0]).abs().max()) <= score + sums
+
+
+@pytest.mark.parametrize("R,n,Hq", [(1, 1, 2), (1, 1, 16), (1, 130, 2)], ids=["one row", "16 rows", "256-row tiles"])
+@pytest.mark.parametrize("up", [7.9, 8.1, 15.9])
+def test_attention_of_scores_that_climb(up, R, n, Hq):
+    """Scores that rise by steps, `up` binary orders in all: numerators against the first keys' maximum reach 2^up,
+    on either side of where the maximum in use is taken anew."""
+    L, page, Hkv = 640, 16, 1
+    k = torch.zeros((L, Hkv, 128), dtype=torch.float16)
+    k[:, 0, 0] = torch.from_numpy(F.E2M1[np.arange(L) * 8 // L])
+    k[:, 0, 1] = 6.0
+    v = torch.from_numpy(np.random.default_rng(0).standard_normal((L, Hkv, 128))).to(torch.float16)
+    pages = vsa.cache_pages(L // page, Hkv, page)
+    vsa.cache_append(k.cuda(), v.cuda(), i32(np.arange(L)), pages)
+    q = torch.zeros((R, n, Hq, 128), dtype=torch.float16, device="cuda")
+    q[..., 0] = up * math.log(2) * math.sqrt(128) / 6
+    q[..., 1] = 30.0
+    table = i32(np.tile(np.arange(L // page), (R, 1)))
+    o, lse = _attend_shared(q, L, page, pages, table, n)
+    vv = F.values(*F.quantise(f64(v)))[:, 0]
+    eo, el, spread, reach = F.attention(f64(q[0, 0, :1]), f64(k[:, 0]), vv, [L])
+    to, tl = F.tolerances(eo, el, spread, reach, L, np.abs(vv).max(), "f16")
+    assert np.all(np.abs(f64(o) - eo[0]) <= to[0])
+    assert np.all(np.abs(f64(lse) - el[0]) <= tl[0])
