@@ -420,7 +420,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
             for (int e = 0; e < 4; ++e) sc[n][u][e] = even[n][e] + odd[n][e];
         }
         // ---- softmax over the keys, in units of 1 / rs (a power of two times log2(e) / sqrt(D))
-        if (key0 + kUnit > lim_min || have != 3) {
+        if (lim_min - key0 < kUnit || have != 3) {  // key0 + kUnit may be 2^31
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const uint2*>(rec + kRecV + (c + 4 * x) * 64 + g * 8);
           uint32_t vs = *reinterpret_cast<const uint32_t*>(rec + kRecVS + g * 16 + c * 4);
-          if (key0 + kUnit > seen || have != 3) {
+          if (seen - key0 < kUnit || have != 3) {
             // behind the last token, or in a record that was not loaded, the scales may be NaN
             const int left = have >> u & 1 ? seen - key0 - 16 * u : 0;
 #pragma unroll

@@ -54,12 +54,16 @@ struct Sched {
     const int last = min((j + 1) * RT, q.n * a.G) - 1;
     return visible(a, q, last / a.G);
   }
+  // Units of n >= 0 keys; n + KT - 1 may pass 2^31.
+  static __device__ __forceinline__ int units_of(int n) {
+    return max(1, static_cast<int>((static_cast<unsigned>(n) + KT - 1) / KT));
+  }
   static __device__ __forceinline__ int units(const AttnArgs& a, const Request& q, int j) {
-    return COST + max(1, (keys(a, q, j) + KT - 1) / KT);
+    return COST + units_of(keys(a, q, j));
   }
   // Places of tiles 0 .. j-1.
   static __device__ __forceinline__ long long units_before(const AttnArgs& a, const Request& q, int j) {
-    if (!a.causal) return static_cast<long long>(COST + max(1, (q.kv + KT - 1) / KT)) * j;
+    if (!a.causal) return static_cast<long long>(COST + units_of(q.kv)) * j;
     if (j <= 1) return j == 0 ? 0 : units(a, q, 0);
     // whole tiles i: the last row's token is floor((RT (i + 1) - 1) / G), it sees kv - n + 1 more than that many
     // tokens, which is floor((RT (i + 1) - 1 + G (kv - n + KT)) / (G KT)) units, or 1 where that is less

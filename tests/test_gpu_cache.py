@@ -743,3 +743,26 @@ def test_attention_of_scores_that_climb(up, R, n, Hq):
     to, tl = F.tolerances(eo, el, spread, reach, L, np.abs(vv).max(), "f16")
     assert np.all(np.abs(f64(o) - eo[0]) <= to[0])
     assert np.all(np.abs(f64(lse) - el[0]) <= tl[0])
+
+
+# ---------------------------------------------------------------------------
+# The longest request
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("n", [1, 66])
+def test_attention_over_the_most_tokens_a_table_row_holds(n):
+    """2^31 - 16 positions, all in one page of 16 tokens: the output is that over the page, the lse more by the log of
+    how often it occurs.  A worker adds fewer than 2^20 products of 16 keys one after another (2^27 of them, 148 workers
+    and more), each sum truncated at 2^-23 of itself: 2^-3; denominators gather fewer terms."""
+    M = (1 << 27) - 1
+    x = torch.from_numpy(np.random.default_rng(4).standard_normal((16, 2, 1, 128)).astype(np.float32)).bfloat16().cuda()
+    pages = vsa.cache_pages(1, 1, 16)
+    vsa.cache_append(x[:, 0], x[:, 1], i32(np.arange(16)), pages)
+    k, v = (F.values(*F.quantise(f64(y)))[:, 0] for y in (x[:, 0], x[:, 1]))
+    q = torch.from_numpy(np.random.default_rng(5).standard_normal((n, 1, 128)).astype(np.float32)).bfloat16().cuda()
+    table = torch.zeros((1, M), dtype=torch.int32, device="cuda")
+    o, lse = vsa.cache_attn(q, i32([0, n]), i32([16 * M]), table, pages, n, vsa.cache_workspace(n, 1, 1), causal=False)
+    eo, el, spread, _ = F.attention(f64(q[:, 0]), k, v, [16] * n)
+    assert np.all(np.abs(f64(lse[:, 0]) - el - math.log(M)) <= 2.0**-3)
+    assert np.all(np.abs(f64(o[:, 0]) - eo) <= 2.0**-3 * spread + 2.0**-8 * np.abs(eo))
