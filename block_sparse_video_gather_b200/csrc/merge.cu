@@ -5,7 +5,8 @@
 // the attention over the union: weights exp(l_i) / (exp(l1) + exp(l2)), lse =
 // log(exp(l1) + exp(l2)).  With m = max(l1, l2), w_i = exp(l_i - m) is in
 // [0, 1] and the larger is 1, so the sum is in [1, 2]; a side of -inf gets
-// weight 0 and its o, which may be anything, is not read into the sum.
+// weight 0 and its o, which may be anything, is not read into the sum.  A NaN in
+// either makes the row NaN.
 // Bound: HBM (two 16-bit reads and one write a channel, 12 bytes a row).  One
 // CTA per (64 tiled rows, b, h), heads the fast index, so that CTAs that run
 // together touch the same tokens' rows; a thread owns one 16-byte chunk of 4
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kTileThreads) untile_merge_kernel(Geo g, int H
     }
   }
   const float m = fmaxf(l1, l2);
-  const bool none = m == -INFINITY;
+  const bool none = l1 == -INFINITY && l2 == -INFINITY;  // by each: fmaxf drops a NaN
   const float w1 = l1 == -INFINITY ? 0.0f : expf(l1 - m);
   const float w2 = l2 == -INFINITY ? 0.0f : expf(l2 - m);
   const float sum = w1 + w2;

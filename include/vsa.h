@@ -563,6 +563,7 @@ VSA_API int vsa_cache_attn_nvfp4(vsa_dtype_t dtype, const uint16_t *q, int64_t q
  *   o, lse             : [B,S,H,D] dtype and [B,S,H] fp32 (lse may be NULL);
  *                        they may be o_past and lse_past themselves
  * lse of -inf: that side has no key and its o is not used; both: o = 0, lse = -inf.
+ * A NaN in either makes the row NaN.
  */
 VSA_API int vsa_untile_merge(vsa_plan_t plan, vsa_dtype_t dtype, const uint16_t *o_tiled, const float *lse_tiled,
                              const uint16_t *o_past, const float *lse_past, int B, int H, int D, uint16_t *o,

@@ -766,3 +766,22 @@ def test_attention_over_the_most_tokens_a_table_row_holds(n):
     eo, el, spread, _ = F.attention(f64(q[:, 0]), k, v, [16] * n)
     assert np.all(np.abs(f64(lse[:, 0]) - el - math.log(M)) <= 2.0**-3)
     assert np.all(np.abs(f64(o[:, 0]) - eo) <= 2.0**-3 * spread + 2.0**-8 * np.abs(eo))
+
+
+# ---------------------------------------------------------------------------
+# The merge of what is not a number
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("which", ["fine", "past"])
+def test_untile_merge_of_nan(which):
+    """A NaN in one lse is a NaN in the result, whether or not the other side has a key."""
+    plan = vsa.Plan(4, 8, 8)
+    ot = torch.ones((1, 1, 256, 128), dtype=torch.bfloat16, device="cuda")
+    past = torch.ones((1, 256, 1, 128), dtype=torch.bfloat16, device="cuda")
+    lt, lp = torch.zeros((1, 1, 256), device="cuda"), torch.zeros((1, 256, 1), device="cuda")
+    own, other = (lt, lp) if which == "fine" else (lp, lt)
+    own.view(-1)[:] = float("nan")
+    other.view(-1)[::2] = -np.inf
+    o, lse = vsa.untile_merge(plan, ot, lt, past, lp)
+    assert torch.isnan(lse).all() and torch.isnan(o).all()
