@@ -37,6 +37,14 @@ constexpr int kMaxRequests = 4096;
 // largest instead of 2^-25: over 126360 tokens a tail there can weigh 4e-3 of a
 // row, and only P V would lose it, not the denominator.
 constexpr float kLift = 7.0f;
+// The longest wait of the attention kernels at one barrier; a call that waited
+// longer ends with VSA_ERR_TIMEOUT.  A test's build sets it to nothing to see
+// the way out; copies in flight are always given kDrainNs to land.
+#ifndef VSA_CACHE_WAIT_NS
+#define VSA_CACHE_WAIT_NS 2000000000
+#endif
+constexpr uint64_t kWaitNs = VSA_CACHE_WAIT_NS;
+constexpr uint64_t kDrainNs = 2000000000;
 
 // Eight fp32 values -> eight E2M1 codes in one word; value 0 in the low nibble
 // of byte 0.  Round to nearest, ties to even, saturate at +-6.

@@ -61,7 +61,6 @@ constexpr uint32_t kSmemK = kSmemQ + 2 * kTileBytes;
 constexpr uint32_t kSmemV = kSmemK + kStagesK * kTileBytes;
 constexpr uint32_t kSmemBar = kSmemV + kStagesV * kTileBytes;
 constexpr uint32_t kSmemTotal = kSmemBar + 512 + 1024;  // barriers, segments + 1 KB alignment slack
-constexpr uint64_t kTimeoutNs = 2000000000ull;          // 2 s per wait
 // Register split: launched at 128 per thread; 128 x (40 + 88) + 256 x 192 = 512 x 128.
 constexpr int kRegsMma = 40, kRegsLoad = 88, kRegsRows = 192;
 static_assert(128 * (kRegsMma + kRegsLoad) + 256 * kRegsRows == kThreads * 128, "register split must match the launch");
@@ -100,7 +99,7 @@ struct Joint {
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Barriers* bars, unsigned int* status) {
-  const bool ok = mbar_wait(bar, parity, &bars->abort, status, kTimeoutNs);
+  const bool ok = mbar_wait(bar, parity, &bars->abort, status, kWaitNs);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Drain: wait for every MMA issued by this thread before TMEM and smem go away.
       mma_commit_w(&bars->drain);
-      mbar_wait_drain(&bars->drain, 0, kTimeoutNs);
+      mbar_wait_drain(&bars->drain, 0, kDrainNs);
     }
   } else if (warp < 8) {
     regs_dec<kRegsLoad>();

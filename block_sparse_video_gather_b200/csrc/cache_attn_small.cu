@@ -49,7 +49,6 @@ using namespace cache;
 
 constexpr int kUnit = 32;                        // keys of a unit: two records
 constexpr int kUnitBytes = 2 * kRecBytes;
-constexpr uint64_t kTimeoutNs = 2000000000ull;   // 2 s per wait
 constexpr int kAtOnce = 16;                      // parts of a row that a warp loads at once when it joins them
 constexpr int kMinUnits = 2;                     // units a warp gets at least
 
@@ -281,11 +280,12 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
       if (__any_sync(0xffffffffu, ready)) {
         idle = 0;
       } else {
-        // bounded like every wait: give up when another warp has, or after 2 s without an emptied stage
+        // bounded like every wait: give up when another warp has, or after kWaitNs without an emptied stage; by
+        // vote, because lanes that read the flag or the clock at different times must not part
         const uint64_t now = globaltimer_ns();
         if (idle == 0) since = now;
         idle = 1;
-        if (*static_cast<volatile int*>(&sm.abort) || now - since > kTimeoutNs) {
+        if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&sm.abort) != 0 || now - since > kWaitNs)) {
           if (lane == 0) {
             sm.abort = 1;
             atomicCAS(a.status, 0u, (unsigned)VSA_ERR_TIMEOUT);
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
           for (int x = 0; x < STAGES; ++x)
             if (mine && issued > x) {
               const int last = issued - 1 - ((issued - 1 - x) % STAGES);
-              mbar_wait_drain(&sm.full[w][x], (last / STAGES) & 1, kTimeoutNs);
+              mbar_wait_drain(&sm.full[w][x], (last / STAGES) & 1, kDrainNs);
             }
           break;
         }
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
         }
       }
 
-      ok = mbar_wait(&sm.full[warp][s], parity, &sm.abort, a.status, kTimeoutNs);
+      ok = mbar_wait(&sm.full[warp][s], parity, &sm.abort, a.status, kWaitNs);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;

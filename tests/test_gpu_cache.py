@@ -785,3 +785,26 @@ def test_untile_merge_of_nan(which):
     other.view(-1)[::2] = -np.inf
     o, lse = vsa.untile_merge(plan, ot, lt, past, lp)
     assert torch.isnan(lse).all() and torch.isnan(o).all()
+
+
+# ---------------------------------------------------------------------------
+# A wait that runs out
+# ---------------------------------------------------------------------------
+
+
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_context_usable(tmp_path, monkeypatch):
+    """The attention for few rows in a build whose longest wait is nothing: its loading warp gives up as soon as no
+    stage is free, the copies under way land, the call ends and reports VSA_ERR_TIMEOUT.  The normal build then gives
+    its results with the workspace zeroed."""
+    b = Batch([1] * 4, [20000] * 4, 8, 8, 64, "bf16")
+    good = b.run(False)
+    variant = vsa_build.build(lib=str(tmp_path / "libvsa_nowait.so"), defines=("VSA_CACHE_WAIT_NS=0",))
+    with monkeypatch.context() as m:
+        m.setattr(vsa, "_lib", None)
+        m.setattr(vsa, "LIB_PATH", variant)
+        b.run(False)
+        assert vsa.get_status() == vsa.VSA_ERR_TIMEOUT
+        assert vsa.get_status() == vsa.VSA_OK  # read and cleared
+    b.ws.zero_()
+    o, lse = b.run(False)
+    assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
