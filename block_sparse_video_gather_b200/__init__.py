@@ -916,27 +916,32 @@ class KVCache:
         self._state = torch.zeros(4 + max_requests, **i32)
         self._start = torch.zeros_like(self._state)
         self.kv_len, self.free_start = self._state[4:], self._state[:1]
+        self._kv_before, self._free_before = self._start[4:], self._start[:1]
         self.cu = torch.zeros(max_requests + 1, **i32)
         self.slots = None
-        self._slots = {}  # by row count: a captured step keeps its own
+        self._captured = {}  # by row count: slots that a captured append reads
+        self._capturing = torch.cuda.is_current_stream_capturing
         self.max_q = max_q
         self.workspace = cache_workspace(max_q, Hq, self.Hkv, device)
 
     def reserve(self, new_len, tokens: int):
         """Room for new_len[r] (int32 [R] on the device) more tokens of each request, `tokens` rows in all with
-        padding; returns their slots."""
-        if tokens not in self._slots:
-            self._slots[tokens] = _torch().empty(tokens, dtype=_torch().int32, device=self.pages.device)
-        self.slots = self._slots[tokens]
+        padding; returns their slots, a tensor of this call's own -- but once append was captured, every later
+        reserve of as many rows writes the tensor that the capture reads."""
+        slots = self._captured.get(tokens)
+        self.slots = self.cu.new_empty(tokens) if slots is None else slots
         self._start.copy_(self._state)
-        cache_tables(self._start[4:], new_len, self.page_tokens, self.free_pages, self._start[:1], self.table,
+        cache_tables(self._kv_before, new_len, self.page_tokens, self.free_pages, self._free_before, self.table,
                      self.slots, kv_len_out=self.kv_len, cu_out=self.cu, free_next_out=self.free_start)
         return self.slots
 
     def append(self, k, v):
-        """Writes k and v [tokens, Hkv, 128] at the slots of the last reserve."""
+        """Writes k and v [tokens, Hkv, 128] at the slots of the last reserve (of the last one called: a replay of
+        a captured step leaves self.slots as it is)."""
         if self.slots is None:
             raise ValueError("reserve comes before append")
+        if self._capturing():
+            self._captured[self.slots.numel()] = self.slots
         cache_append(k, v, self.slots, self.pages)
 
     def attend(self, q, causal: bool = True, cu=None, o_out=None, lse_out=None, max_q: int | None = None):

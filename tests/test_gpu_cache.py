@@ -808,3 +808,53 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_the_context_usable(tmp_path
     b.ws.zero_()
     o, lse = b.run(False)
     assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+
+
+# ---------------------------------------------------------------------------
+# KVCache and Forward(past=)
+# ---------------------------------------------------------------------------
+
+
+def test_reserves_of_many_sizes_keep_no_memory():
+    cache = vsa.KVCache(num_pages=4, Hq=1, page_tokens=16)
+    none = i32([0])
+    cache.reserve(none, 4000)
+    before = torch.cuda.memory_allocated()
+    for tokens in range(4001, 4201):
+        cache.reserve(none, tokens)
+    assert torch.cuda.memory_allocated() - before <= 1 << 16
+
+
+def test_slots_of_a_reserve_are_its_callers():
+    cache = vsa.KVCache(num_pages=4, Hq=1, page_tokens=16)
+    first = cache.reserve(i32([3]), 3)
+    second = cache.reserve(i32([3]), 3)
+    assert first.tolist() != second.tolist()
+    assert vsa.cache_read(first, cache.pages)[0].shape == (3, 1, 128)
+    page = int(cache.table[0, 0])
+    assert [s - 16 * page for s in first.tolist()] == [0, 1, 2] and [s - 16 * page for s in second.tolist()] == [3, 4, 5]
+
+
+def test_a_captured_append_follows_the_reserves_outside():
+    """reserve outside the capture, append inside: each replay writes at the slots of the last reserve of that size,
+    whatever was reserved and allocated between."""
+    cache = vsa.KVCache(num_pages=8, Hq=1, page_tokens=16)
+    k = torch.zeros((2, 1, 128), dtype=torch.bfloat16, device="cuda")
+    cache.reserve(i32([2]), 2)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        cache.append(k, k)
+    g.replay()
+    for i in range(1, 5):
+        cache.reserve(i32([1]), 1)
+        cache.append(k[:1], k[:1])
+        slots = cache.reserve(i32([2]), 2)
+        del slots
+        junk = [torch.full((2,), -1, dtype=torch.int32, device="cuda") for _ in range(50)]
+        k.fill_(6.0 * i)
+        g.replay()
+        at = cache.kv_len.item()
+        last = i32([int(cache.table[0, p // 16]) * 16 + p % 16 for p in (at - 2, at - 1)])
+        assert bool((vsa.cache_read(last, cache.pages)[0] == 6.0 * i).all())
+        del junk
