@@ -32,7 +32,7 @@ SYMBOLS = (
     "vsa_sparse_attn_bwd_workspace", "vsa_sparse_attn_bwd", "vsa_quantize_nvfp4", "vsa_sparse_attn_fwd_nvfp4",
     "vsa_coarse_topk_prefix", "vsa_tile_coarse_prefix", "vsa_sparse_attn_fwd_ws", "vsa_sparse_attn_fwd_nvfp4_ws",
     "vsa_cache_page_bytes", "vsa_cache_tables", "vsa_cache_release", "vsa_cache_append_nvfp4", "vsa_cache_read_nvfp4",
-    "vsa_cache_attn_workspace", "vsa_cache_attn_nvfp4", "vsa_untile_merge",
+    "vsa_cache_attn_workspace", "vsa_cache_attn_nvfp4", "vsa_cache_attn_nvfp4_fill", "vsa_untile_merge",
 )
 
 CACHE_RECORD_BYTES = 2304  # 16 tokens of one head in the 4-bit key/value cache
@@ -101,6 +101,7 @@ def lib():
         L.vsa_cache_read_nvfp4.argtypes = [i, P, i, i, i, P, i, i, P, P, P]
         L.vsa_cache_attn_workspace.argtypes = [i, i, i, P]
         L.vsa_cache_attn_nvfp4.argtypes = [i, P, i64, P, P, i, i, i, i, i, i, P, i, i, P, i, i, P, P, P, P]
+        L.vsa_cache_attn_nvfp4_fill.argtypes = [i, P, i64, P, P, i, i, i, i, i, i, P, i, i, P, i, i, i, P, P, P, P]
         L.vsa_untile_merge.argtypes = [P, i, P, P, P, P, i, i, i, P, P, P]
         L.vsa_get_status.argtypes = [P, P]
         L.vsa_strerror.argtypes = [i]
@@ -649,7 +650,8 @@ def cache_workspace(max_q: int, Hq: int, Hkv: int, device="cuda"):
 def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal: bool = True, o_out=None,
                lse_out=None):
     """Attention of q [T, Hq, 128] (tokens may be strided) over each request's cached tokens -> (o [T, Hq, 128],
-    lse [T, Hq]).  Request r's queries are rows cu[r] .. cu[r+1]; causal: they are the cache's last tokens.
+    lse [T, Hq]).  Request r's queries are rows cu[r] .. cu[r+1]; causal: they are the cache's last tokens.  Rows
+    outside every request are left as they were (0 and -inf in tensors made here).
     workspace: cache_workspace of at least this max_q and these heads; left ready for the next call."""
     dev, stream = _device_and_stream(q, "q")
     torch = _torch_module
@@ -665,19 +667,22 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
     need = _attn_workspace_bytes(Hq, Hkv, max_q)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace needs {need} bytes (cache_workspace)")
+    fill = 0
     if o_out is None:
         o_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        fill = 1
     if lse_out is None:
         lse_out = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        fill |= 2
     if o_out.shape != shape or lse_out.shape != shape[:2]:
         raise ValueError(f"o_out must be [{T}, {Hq}, {D}], lse_out [{T}, {Hq}]")
     if T == 0:
         return o_out, lse_out
     i32 = torch.int32
-    _check(lib().vsa_cache_attn_nvfp4(
+    _check(lib().vsa_cache_attn_nvfp4_fill(
         code, q.data_ptr(), qs, _at(cu, i32, dev, "cu"), _at(kv_len, i32, dev, "kv_len"), R, T, max_q, Hq, Hkv, D,
         _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(block_table, i32, dev, "block_table"),
-        max_pages, int(causal), _at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
+        max_pages, int(causal), fill, _at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
         _at(workspace, workspace.dtype, dev, "workspace"), stream), "vsa_cache_attn_nvfp4")
     return o_out, lse_out
 
@@ -897,7 +902,8 @@ class KVCache:
     Each step: reserve(new_len, tokens) makes room for every request's new tokens, append(k, v) writes them (k, v
     [tokens, Hkv, 128], request after request; rows past the last new token are padding), attend(q, max_q) attends
     over the cache.  release(drop) ends requests.  Nothing synchronises with the host, and a step can be captured
-    in a CUDA graph; a request that does not fit is refused and sets VSA_ERR_CAPACITY (get_status).
+    in a CUDA graph; a request that does not fit is refused and sets VSA_ERR_CAPACITY (get_status).  Its rows stay in
+    the batch: attend gives them what its last cached tokens see, which is of no use.
 
     A video made chunk by chunk: o_past = attend_chunk(q) over the earlier chunks, Forward(q, k, v, past=o_past) over
     the current one, then reserve and append the chunk's k and v.

@@ -132,6 +132,7 @@ struct AttnArgs {
   void* ws;
   unsigned int* status;
   float scale_log2;  // log2(e) / sqrt(D)
+  int fill;          // rows outside every request: 1: o = 0, 2: lse = -inf, 0: left as they were
 };
 
 // A request's new tokens [q0, q0 + n) of the batch and its cached tokens, cut
@@ -148,6 +149,25 @@ __device__ __forceinline__ Request load_request(const AttnArgs& a, int r, bool r
   q.kv = static_cast<int>(min(static_cast<long long>(max(kv, 0)), cap));
   if (report && (q.q0 != c0 || q.q0 + q.n != c1 || q.kv != kv)) atomicCAS(a.status, 0u, (unsigned)VSA_ERR_BAD_INDEX);
   return q;
+}
+
+// The rows before the first request and behind the last, as a.fill says: one
+// pass over them by all threads of the grid.  A call, because inlined it makes
+// the kernel for few rows spill.
+static __device__ __noinline__ void fill_rows(const AttnArgs& a) {
+  const long long before = min(max(__ldg(a.cu), 0), a.T);
+  const long long behind = min(max(static_cast<long long>(__ldg(a.cu + a.R)), before), static_cast<long long>(a.T));
+  const long long rows = before + a.T - behind;
+  const int grid = gridDim.x * gridDim.y, cta = blockIdx.y * gridDim.x + blockIdx.x;
+  const long long first = static_cast<long long>(cta) * blockDim.x + threadIdx.x;
+  const long long step = static_cast<long long>(grid) * blockDim.x;
+  const int chunks = a.Hq * 16;  // of 16 bytes in a row of o
+  if (a.fill & 1)
+    for (long long i = first; i < rows * chunks; i += step)
+      reinterpret_cast<uint4*>(a.o)[i < before * chunks ? i : i + (behind - before) * chunks] = make_uint4(0, 0, 0, 0);
+  if (a.fill & 2)
+    for (long long i = first; i < rows * a.Hq; i += step)
+      a.lse[i < before * a.Hq ? i : i + (behind - before) * a.Hq] = -INFINITY;
 }
 
 // The cached positions that a request's new token i sees: [0, limit).

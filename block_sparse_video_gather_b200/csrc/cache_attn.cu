@@ -33,6 +33,7 @@ cudaError_t launch_cache_attn(const cache::AttnArgs& a, bool f16, int max_q, int
   const int over = a.R == 1 ? 0 : kFewRows;
   cache::AttnArgs b = a;
   b.ws = static_cast<char*>(a.ws) + cache_attn_small_workspace(kWorkers);
+  if (over != 0) b.fill = 0;  // the second kernel does it
   cudaError_t e = launch_cache_attn_chunk(b, over, f16, workers, stream);
   if (e != cudaSuccess || over == 0) return e;
   return launch_cache_attn_small(a, 0, kFewRows, f16, kFewRows, workers, stream);

@@ -741,6 +741,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __shared__ RowSum row_sums[kJoinWarps][kJoinRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * kJoinRows + lane;
+  if (a.fill) fill_rows(a);
   const Joint* joints = static_cast<const Joint*>(a.ws);
   int first = blockIdx.x, quarter = 0;
   if (joints[first].last < 0) {

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
     sm.abort = 0;
     sm.join[0][0] = sm.join[1][0] = -1;
   }
+  if (a.fill) fill_rows(a);
   // the sums over many requests take the place of the warps' pieces until every warp has found its own
   long long* pre = reinterpret_cast<long long*>(&sm.piece[0][0]);
   static_assert(sizeof(sm.piece) >= (kMaxRequests + 1) * 8, "the requests' sums must fit");
@@ -420,7 +421,8 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
             for (int e = 0; e < 4; ++e) sc[n][u][e] = even[n][e] + odd[n][e];
         }
         // ---- softmax over the keys, in units of 1 / rs (a power of two times log2(e) / sqrt(D))
-        if (lim_min - key0 < kUnit || have != 3) {  // key0 + kUnit may be 2^31
+        const unsigned key1 = key0 + static_cast<unsigned>(kUnit);  // may be 2^31
+        if (key1 > static_cast<unsigned>(lim_min) || have != 3) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) w[x] = *reinterpret_cast<const uint2*>(rec + kRecV + (c + 4 * x) * 64 + g * 8);
           uint32_t vs = *reinterpret_cast<const uint32_t*>(rec + kRecVS + g * 16 + c * 4);
-          if (seen - key0 < kUnit || have != 3) {
+          if (key1 > static_cast<unsigned>(seen) || have != 3) {
             // behind the last token, or in a record that was not loaded, the scales may be NaN
             const int left = have >> u & 1 ? seen - key0 - 16 * u : 0;
 #pragma unroll

@@ -685,11 +685,20 @@ int vsa_cache_attn_nvfp4(vsa_dtype_t dtype, const uint16_t* q, int64_t q_stride,
                          const int32_t* kv_len, int R, int T, int max_q, int Hq, int Hkv, int D, const uint8_t* pages,
                          int num_pages, int page_tokens, const int32_t* block_table, int max_pages, int causal,
                          uint16_t* o, float* lse, void* workspace, vsa_stream_t stream) {
+  return vsa_cache_attn_nvfp4_fill(dtype, q, q_stride, cu, kv_len, R, T, max_q, Hq, Hkv, D, pages, num_pages,
+                                   page_tokens, block_table, max_pages, causal, 0, o, lse, workspace, stream);
+}
+
+int vsa_cache_attn_nvfp4_fill(vsa_dtype_t dtype, const uint16_t* q, int64_t q_stride, const int32_t* cu,
+                              const int32_t* kv_len, int R, int T, int max_q, int Hq, int Hkv, int D,
+                              const uint8_t* pages, int num_pages, int page_tokens, const int32_t* block_table,
+                              int max_pages, int causal, int fill, uint16_t* o, float* lse, void* workspace,
+                              vsa_stream_t stream) {
   if (dtype != VSA_BF16 && dtype != VSA_F16) return VSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cu) || !aligned16(kv_len) || !aligned16(pages) || !aligned16(block_table) ||
       !aligned16(o) || !aligned16(lse) || !aligned16(workspace))
     return VSA_ERR_INVALID_ARG;
-  if (R < 1 || T < 0 || max_q < 1 || Hq < 1 || max_pages < 1) return VSA_ERR_INVALID_ARG;
+  if (R < 1 || T < 0 || max_q < 1 || Hq < 1 || max_pages < 1 || fill < 0 || fill > 3) return VSA_ERR_INVALID_ARG;
   if (int rc = check_cache(Hkv, D, num_pages, page_tokens)) return rc;
   if (Hq % Hkv != 0 || q_stride < static_cast<int64_t>(Hq) * D || (q_stride & 7)) return VSA_ERR_INVALID_ARG;
   if (R > vsa::cache::kMaxRequests) return VSA_ERR_UNSUPPORTED;
@@ -718,6 +727,7 @@ int vsa_cache_attn_nvfp4(vsa_dtype_t dtype, const uint16_t* q, int64_t q_stride,
   a.ws = workspace;
   a.status = ds->status;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / 11.313708498984761);  // log2(e) / sqrt(128)
+  a.fill = fill;
   return from_cuda(vsa::launch_cache_attn(a, dtype == VSA_F16, max_q, ds->num_sms,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -522,7 +522,10 @@ VSA_API int vsa_cache_read_nvfp4(vsa_dtype_t dtype, const int32_t *slots, int T,
  *   o = sum_j softmax_j(D^-1/2 q . k_j) v_j,   lse = log sum_j exp(D^-1/2 q . k_j)
  * with j < kv_len[r], and with causal != 0 also j <= kv_len[r] - n_r + i (the
  * new tokens are the cache's last n_r).  A row that sees no position gives
- * o = 0 and lse = -inf.
+ * o = 0 and lse = -inf.  Lengths are taken as they stand: a request that
+ * vsa_cache_tables refused still has its rows in cu over its old kv_len, and
+ * with causal != 0 these see what its last tokens see, although they are not
+ * in the cache; the status word is what tells.
  *   q        : [T, Hq, D] dtype, q_stride elements from token to token (at
  *              least Hq * D, a multiple of 8)
  *   cu       : [R + 1] int32, ascending within [0, T];  kv_len: [R] int32
@@ -530,7 +533,7 @@ VSA_API int vsa_cache_read_nvfp4(vsa_dtype_t dtype, const int32_t *slots, int T,
  *   max_q    : the largest n_r, or an upper bound: it selects the kernel, and
  *              a bound that does not hold costs speed, not results
  *   o        : [T, Hq, D] dtype, lse: [T, Hq] fp32; rows outside every
- *              request are left as they were
+ *              request are left as they were (the form below writes them)
  *   workspace: vsa_cache_attn_workspace bytes, zero before the first call;
  *              each call leaves its counters zero unless it reports
  *              VSA_ERR_TIMEOUT, after which the caller zeroes it again.  Calls
@@ -550,6 +553,16 @@ VSA_API int vsa_cache_attn_nvfp4(vsa_dtype_t dtype, const uint16_t *q, int64_t q
                                  const uint8_t *pages, int num_pages, int page_tokens, const int32_t *block_table,
                                  int max_pages, int causal, uint16_t *o, float *lse, void *workspace,
                                  vsa_stream_t stream);
+
+/*
+ * The same, and the rows before cu[0] and from cu[R] on (a padded batch) are
+ * written too: fill & 1: o = 0, fill & 2: lse = -inf.
+ */
+VSA_API int vsa_cache_attn_nvfp4_fill(vsa_dtype_t dtype, const uint16_t *q, int64_t q_stride, const int32_t *cu,
+                                      const int32_t *kv_len, int R, int T, int max_q, int Hq, int Hkv, int D,
+                                      const uint8_t *pages, int num_pages, int page_tokens,
+                                      const int32_t *block_table, int max_pages, int causal, int fill, uint16_t *o,
+                                      float *lse, void *workspace, vsa_stream_t stream);
 
 /*
  * Untile fused with the merge of the fine stage and an attention over other

@@ -135,3 +135,13 @@ def test_plain_forms_round_to_nearest_even_and_invert():
 def test_plain_attention_of_a_row_without_keys():
     o, lse, _, _ = F.attention(np.ones((2, 128)), np.ones((3, 128)), np.ones((3, 128)), [0, 2])
     assert np.all(o[0] == 0) and lse[0] == -np.inf and np.allclose(o[1], 1)
+
+
+def test_the_filling_attention_refuses_what_the_other_does(L):
+    good, bad = _calls(L)["vsa_cache_attn_nvfp4"]
+    at = lambda pos: pos + (pos >= 17)  # `fill` comes after `causal`
+    cases = [(at(pos), value, code) for pos, values in bad.items() for value, code in values]
+    for pos, value, code in cases + [(17, -1, INV), (17, 4, INV)]:
+        args = good[:17] + [3] + good[17:]
+        args[pos] = value
+        assert L.vsa_cache_attn_nvfp4_fill(*args) == code, (pos, value)

@@ -858,3 +858,45 @@ def test_a_captured_append_follows_the_reserves_outside():
         last = i32([int(cache.table[0, p // 16]) * 16 + p % 16 for p in (at - 2, at - 1)])
         assert bool((vsa.cache_read(last, cache.pages)[0] == 6.0 * i).all())
         del junk
+
+
+@pytest.mark.parametrize("n,kv", [([2, 1], [40, 20]), ([100], [300]), ([100, 2], [300, 40])],
+                         ids=["few rows", "many", "both"])
+def test_rows_outside_every_request_in_tensors_made_here(n, kv):
+    """Rows before and behind the requests of a result that the call makes itself: o = 0, lse = -inf; in a tensor that
+    the caller gives they stay."""
+    b = Batch(n, kv, 4, 2, 16, "bf16", pad_rows=8)
+    T, first, behind = b.T, 3, 3 + sum(n)
+    want = b.run(True)
+    q = torch.cat([b.q[:first], b.q[:T - first]])
+    args = (q, i32(b.cu + first), i32(kv), i32(b.table), b.pages, max(n), b.ws)
+    for keep in ((), ("o_out",), ("lse_out",)):
+        junk = [torch.full((T, 4, 128), float("nan"), dtype=torch.bfloat16, device="cuda"),
+                torch.full((T, 4), float("nan"), device="cuda")]
+        given = dict(o_out=junk[0].clone().fill_(7.0), lse_out=junk[1].clone().fill_(7.0))
+        given = {name: given[name] for name in keep}
+        del junk
+        o, lse = vsa.cache_attn(*args, **given)
+        assert torch.equal(o[first:behind], want[0][:sum(n)]) and torch.equal(lse[first:behind], want[1][:sum(n)])
+        for x, name, value in ((o, "o_out", 0.0), (lse, "lse_out", -np.inf)):
+            outside = torch.cat([x[:first], x[behind:]])
+            assert outside.shape[0] == T - sum(n) and bool((outside == (7.0 if name in keep else value)).all())
+
+
+def test_rows_of_a_request_that_was_refused():
+    """A request that reserve refuses keeps its length; its rows of the batch see what its last tokens see."""
+    cache = vsa.KVCache(num_pages=3, Hq=1, max_requests=2, page_tokens=16, max_q=8)
+    x = torch.randn((40, 1, 128), device="cuda").bfloat16()
+    cache.reserve(i32([16, 10]), 26)
+    cache.append(x[:26], x[:26])
+    cache.reserve(i32([17, 6]), 23)  # two pages where one is left; none
+    assert vsa.get_status() == vsa.VSA_ERR_CAPACITY
+    cache.append(x[:23], x[:23])
+    assert cache.kv_len.tolist() == [16, 16] and cache.cu.tolist() == [0, 17, 23]
+    assert bool((cache.slots[:17] == -1).all()) and bool((cache.slots[17:] >= 0).all())
+    q = torch.randn((23, 1, 128), device="cuda").bfloat16()
+    o, lse = cache.attend(q)
+    kv, cu = i32([16, 16]), i32([0, 17, 23])
+    o2, lse2 = vsa.cache_attn(q, cu, kv, cache.table, cache.pages, 8, vsa.cache_workspace(8, 1, 1))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert not o[0].any() and bool(torch.isneginf(lse[0]).all())  # 17 rows over 16 tokens: the first sees none
