@@ -851,6 +851,19 @@ class Forward:
         self.quantize()
         self.attend()
 
+    def check_past(self, past):
+        """Refuses a past that does not fit, before anything is launched."""
+        if self.gated:
+            raise ValueError("past applies to a Forward without the gate-compress branch")
+        o_past, lse_past = past
+        shape = (self.B, self.plan.S, self.H, self.D)
+        if o_past.shape != shape or lse_past.shape != shape[:3]:
+            raise ValueError(f"past must be o {shape} and lse {shape[:3]}, got {tuple(o_past.shape)} and "
+                             f"{tuple(lse_past.shape)}")
+        dev = self.ot.get_device()
+        _at(o_past, self.ot.dtype, dev, "o_past")
+        _at(lse_past, self.lse.dtype, dev, "lse_past")
+
     def back(self, gate=None, out=None, past=None):
         out = self.o if out is None else out
         if past is not None:
@@ -868,6 +881,8 @@ class Forward:
         """One forward step; o goes to `out` when given (else to self.o)."""
         if self.gated != (gate is not None):
             raise ValueError("a gate is required exactly when the Forward was built with gated=True")
+        if past is not None:
+            self.check_past(past)
         self.front(q, k, v, block_map, row_keep)
         self.fine()
         o = self.back(gate, out, past)
@@ -877,7 +892,8 @@ class Forward:
         """Capture one forward step on these device tensors in a CUDA graph and
         return it (torch.cuda.CUDAGraph); replay() reruns the step's launches
         with the inputs read from the same buffers and o / lse written to
-        self.o / self.lse.  One eager step runs first so that every host-side
+        self.o / self.lse (with a past the lse over both key sets to
+        self.lse_all).  One eager step runs first so that every host-side
         set-up (device state, tensor-map encoder, kernel attributes) happens
         outside the capture."""
         torch = _torch()

@@ -900,3 +900,25 @@ def test_rows_of_a_request_that_was_refused():
     o2, lse2 = vsa.cache_attn(q, cu, kv, cache.table, cache.pages, 8, vsa.cache_workspace(8, 1, 1))
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert not o[0].any() and bool(torch.isneginf(lse[0]).all())  # 17 rows over 16 tokens: the first sees none
+
+
+def _chunk(plan, H, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [torch.randn((1, plan.S, H, 128), generator=g, device="cuda").bfloat16() for _ in range(3)]
+
+
+def test_forward_refuses_a_past_before_it_launches_anything():
+    plan, H = vsa.Plan(4, 8, 8), 1
+    q, k, v = _chunk(plan, H, 3)
+    past = (torch.zeros_like(q), torch.zeros((1, plan.S, H), device="cuda"))
+    fwd, gated = vsa.Forward(plan, 1, H, 1), vsa.Forward(plan, 1, H, 1, gated=True)
+    for f in (fwd, gated):
+        f.ot.fill_(7.0)
+    with pytest.raises(ValueError, match="past"):
+        gated(q, k, v, gate=q, past=past)
+    for bad in ((past[0][:, :-1], past[1]), (past[0], past[1][:, :-1]), (past[0].half(), past[1]),
+                (past[0], past[1].double()), (past[0].cpu(), past[1])):
+        with pytest.raises(ValueError):
+            fwd(q, k, v, past=bad)
+    torch.cuda.synchronize()
+    assert bool((fwd.ot == 7.0).all()) and bool((gated.ot == 7.0).all())
