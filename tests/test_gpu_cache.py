@@ -922,3 +922,73 @@ def test_forward_refuses_a_past_before_it_launches_anything():
             fwd(q, k, v, past=bad)
     torch.cuda.synchronize()
     assert bool((fwd.ot == 7.0).all()) and bool((gated.ot == 7.0).all())
+
+
+FORMS = {"256": (dict(T=4, Hg=9, Wg=10), {}, {}), "nvfp4": (dict(T=4, Hg=9, Wg=10), {}, dict(nvfp4=True)),
+         "64": (dict(T=4, Hg=8, Wg=12), dict(block=(4, 4, 4), n_prefix=70), dict(prefix_dense=True)),
+         "64 nvfp4": (dict(T=4, Hg=8, Wg=12), dict(block=(4, 4, 4), n_prefix=70), dict(prefix_dense=True, nvfp4=True))}
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_forward_with_a_past_in_each_form(form):
+    """fwd(past=) is the fine stage's result merged with the past, eager and as Forward.graph captures it."""
+    grid, layout, kind = FORMS[form]
+    plan, H = vsa.Plan(*grid.values(), **layout), 2
+    q, k, v = _chunk(plan, H, 1)
+    past = (torch.randn_like(q), torch.randn((1, plan.S, H), device="cuda") + 4)
+    plain = vsa.Forward(plan, 1, H, 2, **kind)
+    plain(q, k, v)
+    o_fine = vsa.untile(plan, plain.ot)
+    l_fine = vsa.untile(plan, plain.lse[..., None].expand(-1, -1, -1, 128).to(torch.bfloat16).contiguous())[..., 0]
+    want = vsa.untile_merge(plan, plain.ot, plain.lse, *past)
+    w = torch.sigmoid(past[1] - l_fine.float())[..., None]  # weight of the past; l_fine is rounded to 8 bits
+    near = (1 - w) * o_fine.float() + w * past[0].float()
+    assert float((want[0].float() - near).abs().max()) <= 2.0**-5 * float(past[0].abs().max())
+    fwd = vsa.Forward(plan, 1, H, 2, **kind)
+    o, lse = fwd(q, k, v, past=past)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    g = fwd.graph(q, k, v, past=past)
+    q2, k2, v2 = _chunk(plan, H, 2)
+    for a, b in zip((q, k, v), (q2, k2, v2)):
+        a.copy_(b)
+    past[1].add_(1.5)
+    g.replay()
+    plain(q, k, v)
+    want = vsa.untile_merge(plan, plain.ot, plain.lse, *past)
+    assert torch.equal(fwd.o, want[0]) and torch.equal(fwd.lse_all, want[1])
+
+
+def test_a_captured_step_of_a_video():
+    """attend_chunk, Forward(past=), reserve and append of one chunk in a graph, replayed chunk after chunk, give the
+    bits of the eager calls."""
+    plan, H = vsa.Plan(4, 9, 10), 2
+
+    def new():
+        return vsa.Forward(plan, 1, H, 2), vsa.KVCache(num_pages=40, Hq=H, max_len=4 * plan.S, max_q=plan.S)
+
+    def step(fwd, cache, q, k, v, n):
+        o, lse = fwd(q, k, v, past=cache.attend_chunk(q))
+        cache.reserve(n, plan.S)
+        cache.append(k[0], v[0])
+        return o, lse
+
+    (fe, ce), (fg, cg) = new(), new()
+    n = i32([plan.S])
+    q, k, v = _chunk(plan, H, 0)
+    step(*new(), q, k, v, n)  # one-time set-up
+    fg(q, k, v)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        og, lg = step(fg, cg, q, k, v, n)
+    for chunk in range(4):
+        for a, b in zip((q, k, v), _chunk(plan, H, 10 + chunk)):
+            a.copy_(b)
+        g.replay()
+        oe, le = step(fe, ce, q, k, v, n)
+        assert torch.equal(og, oe) and torch.equal(lg, le)
+        assert torch.equal(cg.kv_len, ce.kv_len) and torch.equal(cg.table, ce.table)
+    pos = torch.arange(4 * plan.S, device="cuda")
+    slots = (ce.table[0, pos // 64] * 64 + pos % 64).int()
+    for a, b in zip(vsa.cache_read(slots, cg.pages), vsa.cache_read(slots, ce.pages)):
+        assert torch.equal(a, b)
