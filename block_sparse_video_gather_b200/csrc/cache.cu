@@ -404,8 +404,9 @@ cudaError_t launch_cache_tables(const CacheTablesArgs& a, int num_sms, cudaStrea
   const int grid = static_cast<int>(passes < 1 ? 1 : passes < num_sms ? passes : num_sms);
   const int smem = 4 * (spread(a.R) + 1) * 4;
   if (smem > 40 * 1024) {  // more than the default limit only for R > 2275
-    cudaError_t e = cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         4 * (spread(kMaxRequests) + 1) * 4);
+    static SmemAllowed allowed;
+    const cudaError_t e =
+        allowed.ensure(reinterpret_cast<const void*>(cache_tables_kernel), 4 * (spread(kMaxRequests) + 1) * 4);
     if (e != cudaSuccess) return e;
   }
   cache_tables_kernel<<<grid, threads, smem, stream>>>(a);
