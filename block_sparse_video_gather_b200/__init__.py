@@ -571,11 +571,13 @@ def cache_tables(kv_len, new_len, page_tokens: int, free_pages, free_start, bloc
 
 def cache_release(drop, page_tokens: int, kv_len, block_table, free_pages, free_start):
     """Gives the pages of the requests with drop[r] != 0 back to the stack and sets their kv_len to 0, in place."""
+    R = kv_len.numel()
+    if kv_len.dim() != 1 or drop.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("drop and kv_len must be [R], block_table [R, max_pages]")
+    if free_start.numel() < 1:
+        raise ValueError("free_start must hold 1 entry")
     dev, stream = _device_and_stream(kv_len, "kv_len")
     i32 = _torch_module.int32
-    R = kv_len.shape[0]
-    if drop.shape != (R,) or block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("drop and kv_len must be [R], block_table [R, max_pages]")
     u8 = _torch_module.uint8
     d = drop.view(u8) if drop.dtype == _torch_module.bool else drop
     _check(lib().vsa_cache_release(

@@ -145,3 +145,16 @@ def test_the_filling_attention_refuses_what_the_other_does(L):
         args = good[:17] + [3] + good[17:]
         args[pos] = value
         assert L.vsa_cache_attn_nvfp4_fill(*args) == code, (pos, value)
+
+
+def test_release_refuses_wrong_shapes(L):
+    kv, table, one = torch.zeros(3, dtype=torch.int32), torch.zeros((3, 4), dtype=torch.int32), torch.ones(3).bool()
+    good = dict(drop=one, kv_len=kv, block_table=table, free_pages=kv, free_start=kv[:1])
+    for name, value, match in (("kv_len", kv.view(3, 1), r"\[R\]"), ("kv_len", table, r"\[R\]"),
+                               ("kv_len", kv[0], r"\[R\]"), ("drop", one[:2], r"\[R\]"),
+                               ("block_table", table[:2], r"\[R\]"), ("block_table", kv, r"\[R\]"),
+                               ("free_start", kv[:0], "free_start")):
+        with pytest.raises(ValueError, match=match):
+            vsa.cache_release(page_tokens=16, **{**good, name: value})
+    with pytest.raises(ValueError, match="CUDA"):
+        vsa.cache_release(page_tokens=16, **good)
