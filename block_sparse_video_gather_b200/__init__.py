@@ -588,7 +588,7 @@ def cache_release(drop, page_tokens: int, kv_len, block_table, free_pages, free_
 
 def cache_append(k, v, slots, pages):
     """Quantises k and v [T, Hkv, 128] bf16/fp16 (tokens may be strided) into the cache at their slots
-    (negative: not written)."""
+    (negative: not written).  Blocks of 16 channels within +-0.0059 are stored as zeros, values beyond 2688 saturate."""
     n, Hkv, page_tokens = _pages_shape(pages)
     code = _dtype_code(k, "k")
     shape = k.shape
@@ -916,6 +916,8 @@ class Forward:
 
 class KVCache:
     """A 4-bit key/value cache of up to max_requests requests, its lengths and free pages kept on the device.
+
+    max_len: the most tokens of a request, rounded up to whole pages (default: every page).
 
     Each step: reserve(new_len, tokens) makes room for every request's new tokens, append(k, v) writes them (k, v
     [tokens, Hkv, 128], request after request; rows past the last new token are padding), attend(q, max_q) attends

@@ -499,7 +499,10 @@ VSA_API int vsa_cache_release(const uint8_t *drop, int R, int page_tokens, int32
  *           written.  Slots of one call must differ: where two tokens share
  *           one, which bytes of each remain is unspecified.
  * Values beyond 2688 = 448 * 6 in magnitude saturate, infinities too; a NaN is
- * stored as some finite value.  T = 0 does nothing.
+ * stored as some finite value.  There is no scale per tensor: 16 channels whose
+ * largest magnitude is 6 * 2^-10 (0.0059) or less round to the scale 0 and are
+ * stored as zeros, so keys and values as small as that are to be scaled up by
+ * the caller.  T = 0 does nothing.
  * A slot >= num_pages * page_tokens is not written and sets VSA_ERR_BAD_INDEX.
  */
 VSA_API int vsa_cache_append_nvfp4(vsa_dtype_t dtype, const uint16_t *k, const uint16_t *v, int64_t k_stride,

@@ -992,3 +992,18 @@ def test_a_captured_step_of_a_video():
     slots = (ce.table[0, pos // 64] * 64 + pos % 64).int()
     for a, b in zip(vsa.cache_read(slots, cg.pages), vsa.cache_read(slots, ce.pages)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_append_of_the_smallest_blocks(dtype):
+    """A block whose largest magnitude is 6 x 2^-10 or less has no scale and is stored as zeros; the next larger value
+    of either type has one."""
+    edge = 6 * 2.0**-10
+    up = edge + 2.0**-8 * torch.finfo(TDT[dtype]).eps
+    x = torch.zeros((2, 1, 128), dtype=TDT[dtype])
+    x[0], x[1] = edge, up
+    pages = vsa.cache_pages(1, 1, 16).fill_(0xA5)
+    vsa.cache_append(x.cuda(), -x.cuda(), i32([0, 1]), pages)
+    k, v = vsa.cache_read(i32([0, 1]), pages, TDT[dtype])
+    assert not f64(k)[0].any() and not f64(v)[0].any()
+    assert np.all(f64(k)[1] == 6 * 2.0**-9 * 0.5) and np.all(f64(v)[1] == -6 * 2.0**-9 * 0.5)
