@@ -22,9 +22,9 @@ using namespace cache;
 // itself in shared memory -- R <= 4096 lengths are 32 KB out of L2 -- and then
 // fills its share of the slots and of the new table entries, finding the
 // request by bisection; so the call is one launch with nothing to wait for.
-// The bound is latency: the largest call writes some MB.  8 requests 4.4 us, 4096
-// requests with 1.02 M new tokens 11.8 us, of which the slots take half (four CTAs'
-// worth of passes side by side, or eight tokens a thread, were slower).
+// The bound is latency: the largest call writes some MB.  8 requests 4.4 to 5.0 us,
+// 4096 requests with 1.02 M new tokens 11.9 to 12.3 us, of which the slots take half
+// (four CTAs' worth of passes side by side, or eight tokens a thread, were slower).
 
 // Threads of a CTA: with many requests the sums and look-ups of a thread are a
 // chain, and twice the threads shorten it (4096 requests 11.8 us, 13.9 with 512);
@@ -52,8 +52,10 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part) {
   return v + (warp > 0 ? before : 0);
 }
 
-// Place of entry i of an array in shared memory: with 8 entries a thread (4096
-// requests) neighbouring threads start 9 words apart, in different banks.
+// Place of entry i of an array in shared memory: neighbouring threads of the
+// release, with 8 entries each at 4096 requests, start 9 words apart, in different
+// banks; those of the tables, twice as many with 4 entries, 4 or 5 words, two to a
+// bank.
 __host__ __device__ constexpr int spread(int i) { return i + (i >> 3); }
 
 // Largest i in [0, n) with a[i] <= x, given a[0] <= x.

@@ -3,11 +3,10 @@
 // requests of an attention call.
 //
 // The cache holds keys and values as NVFP4, the format of the fine stage's
-// quantised Q and K (fp4.cu; FastVideo "Optimizations" page, section "FP4 Flash
-// Attention 4 (Blackwell only)"): E2M1 codes and one E4M3 scale per 16
-// channels.  16 tokens of one page and head are one record of 2304 contiguous
-// bytes, so that a kernel fetches the keys, the values and their scales of 16
-// tokens with one bulk copy whatever the page size:
+// quantised Q and K (fp4.cu): E2M1 codes and one E4M3 scale per 16 channels.
+// 16 tokens of one page and head are one record of 2304 contiguous bytes, so
+// that a kernel fetches the keys, the values and their scales of 16 tokens with
+// one bulk copy whatever the page size:
 //   [   0,1024)  K codes, 64 B per token
 //   [1024,2048)  V codes, 64 B per token
 //   [2048,2176)  K scales, byte 8 t + g

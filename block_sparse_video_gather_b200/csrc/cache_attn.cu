@@ -10,10 +10,18 @@ constexpr int kWorkers = 160;  // CTAs of a call at most: one per SM, B200 has 1
 
 // Requests of up to this many rows (new tokens times query heads of a key head)
 // run the kernel for few rows, others the 256-row tiles of the tensor cores.
-// Measured over 8000 cached tokens, us, few rows / tensor cores: 1 request x 12
-// heads, 40 rows 30.3 / 32.6, 64 rows 34.1 / 32.7; 9 requests of up to 64 rows x
-// 3 heads 38.7 / 57.0, 32 x 8 heads 200 / 210 (some of their requests have fewer
-// rows, so that with a lower border both kernels run).
+// Measured over 8000 cached tokens, causal, 4 query heads a key head, us on the
+// device, the whole batch on few rows / on tensor cores:
+//   requests x heads     24 rows     40 rows     64 rows     96 rows
+//   1 x 12             23.7/26.8   30.1/27.5   33.3/27.5   41.2/28.2
+//   9 x 3              33.5/41.0   44.9/41.4   52.8/41.6   71.7/42.6
+//   32 x 8               186/293     272/294     358/295     526/298
+//   9 x 3, ragged      29.4/41.0   33.3/41.2   41.4/41.6   53.3/42.5
+//   32 x 8, ragged       133/292     171/293     231/294     327/295
+// (ragged: lengths spread below the given one).  Even batches cross between 24 and
+// 50 rows, ragged ones between 64 and 90.  One border serves both, and it lies where
+// ragged batches cross, which are the usual ones; from there on a ragged batch runs
+// both kernels in line (96 rows: 9 x 3 61.5, 32 x 8 281).
 constexpr int kFewRows = 64;
 
 }  // namespace

@@ -22,12 +22,12 @@
 //   warps 4-7    K and V tiles from codes: a thread 32 channels of 4 keys
 //   warps 8-11   rows of query tile 0: Q, softmax, output
 //   warps 12-15  rows of query tile 1
-// Bound: the rows' threads (a tile's softmax, then the products that wait for
-// it), as in the fine stage; the conversion (256 values a key and CTA, whatever
-// its rows) runs beside it and waits a quarter of its time.  6240 tokens over
-// 32760, 12 heads: 1.29 to 1.35 ms, 930 to 970 TFLOP/s of 16-bit products where the fine stage
-// does 970 to 990.  Every fourth exponential by a polynomial was 7% slower: the
-// issue slots, not ex2, are what the rows' threads share with the conversion.
+// Bound: no one unit is full (tensor pipe 42%, issue slots 42%).  A tile's
+// softmax and the products that wait for it are a chain, as in the fine stage,
+// and the conversion (256 values a key and CTA, whatever its rows) takes issue
+// slots beside it: 6240 tokens over 32760, 12 heads, run in 1.29 to 1.35 ms, 930
+// to 970 TFLOP/s of 16-bit products, 6 to 11% below the fine stage (1006 to
+// 1049).  Every fourth exponential by a polynomial was 7% slower.
 //
 // An item cut between CTAs leaves its rows' sums, maxima and denominators in
 // the workspace, and a second kernel joins them in the order of the line.
@@ -48,7 +48,7 @@ constexpr int kThreads = 512;
 constexpr int kRowTile = 256, kKeyTile = 128;
 constexpr int kStagesK = 3, kStagesV = 2, kSegs = 4;
 // An item's rows of Q, first product and output take a CTA some 6 to 9 us, a unit 2.4 us (4 x 1023 on 5000: 157 us with
-// 4, 162 with 3, 170 with 2, 196 with 0, a pass; one long item does not care).
+// 4, 162 with 3, 170 with 2, 196 with 0, a pass; one long item does not care).  Measured on that one shape only.
 constexpr int kItemCost = 4;
 // Places of the line that a CTA gets at least.  Shorter shares end sooner but have more parts to join: 3 requests of
 // 78 rows on 1483, 8 heads, 58.2 us with 8, 50.8 with 4, 45.3 with 2; one of 61 x 3 rows on 19525 32.3 with 4, 34.5

@@ -1,14 +1,16 @@
 // cache_attn_small.cu -- attention over the 4-bit cache for few rows a request:
 // a decoded token, or some drafted ones.
 //
-// Bound: HBM on paper, the issue slots beside it.  A cached token and head are
-// 144 bytes, 0.022 ns at 6561 GB/s; the work beside the loads is to make 256
-// fp16 values of them, some 290 warp instructions per 16 tokens.  126360 tokens
-// x 12 heads: 50 us, 4.3 TB/s; a copy that only loads took 46 of the 57 us before
-// the loads had a warp of their own, about 10 of them the launch, finding the
-// place, the first loads and the joins.  A single token over 777 is 10 us, nearly
-// all of it those.  Adding a unit's values beside the next one's scores and units
-// of 16 tokens were no faster.  What the design does:
+// Bound: HBM on paper, latency in fact.  A cached token and head are 144 bytes,
+// 0.022 ns at 6561 GB/s; the work beside the loads is to make 256 fp16 values of
+// them, some 290 warp instructions per 16 tokens.  126360 tokens x 12 heads: 51 us,
+// 4.3 TB/s, two thirds of HBM, with 0.55 instructions issued a cycle and scheduler
+// and no pipe above half.  About 10 us of it are the launch, finding the place, the
+// first loads and the joins, which are nearly all of the 10 us of a single token
+// over 777; in the rest a unit is a chain (wait, scores, vote, exponentials,
+// transposes, products) on the four warps of a scheduler.  Adding a unit's values
+// beside the next one's scores and units of 16 tokens were no faster.  What the
+// design does:
 //  - The line of 32-token units (cache_sched.cuh) is cut evenly over the CTAs,
 //    one per SM, and a CTA's share evenly over its warps.  A warp works alone:
 //    its own ring of units (a bulk copy of 4608 bytes each, or two where a page

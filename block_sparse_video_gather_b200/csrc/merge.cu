@@ -13,7 +13,8 @@
 // rows, all loaded at once.  A row's weights are made by one lane for its 16
 // threads: with two exponentials, a logarithm and a quotient in every thread
 // the arithmetic took longer than the traffic (64 us for the 306 MB of a
-// (21, 30, 52) grid and 12 heads; now 52, 5.9 TB/s).
+// (21, 30, 52) grid and 12 heads; now 52.7 alone, 54.7 with the next call behind
+// it, 5.6 to 5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
