@@ -681,11 +681,15 @@ def cache_attn(q, cu, kv_len, block_table, pages, max_q: int, workspace, causal:
     if T == 0:
         return o_out, lse_out
     i32 = torch.int32
-    _check(lib().vsa_cache_attn_nvfp4_fill(
-        code, q.data_ptr(), qs, _at(cu, i32, dev, "cu"), _at(kv_len, i32, dev, "kv_len"), R, T, max_q, Hq, Hkv, D,
-        _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(block_table, i32, dev, "block_table"),
-        max_pages, int(causal), fill, _at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
-        _at(workspace, workspace.dtype, dev, "workspace"), stream), "vsa_cache_attn_nvfp4")
+    before = (code, q.data_ptr(), qs, _at(cu, i32, dev, "cu"), _at(kv_len, i32, dev, "kv_len"), R, T, max_q, Hq, Hkv, D,
+              _at(pages, torch.uint8, dev, "pages"), n, page_tokens, _at(block_table, i32, dev, "block_table"),
+              max_pages, int(causal))
+    after = (_at(o_out, q.dtype, dev, "o"), _at(lse_out, torch.float32, dev, "lse"),
+             _at(workspace, workspace.dtype, dev, "workspace"), stream)
+    if fill:
+        _check(lib().vsa_cache_attn_nvfp4_fill(*before, fill, *after), "vsa_cache_attn_nvfp4_fill")
+    else:
+        _check(lib().vsa_cache_attn_nvfp4(*before, *after), "vsa_cache_attn_nvfp4")
     return o_out, lse_out
 
 

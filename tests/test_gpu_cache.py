@@ -4,6 +4,7 @@ Block tables and slots, codes and scales are whole numbers and compared exactly;
 bounds derived at cache_forms.tolerances and below.
 """
 import math
+import os
 
 import numpy as np
 import pytest
@@ -796,6 +797,8 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_the_context_usable(tmp_path
     """The attention for few rows in a build whose longest wait is nothing: its loading warp gives up as soon as no
     stage is free, the copies under way land, the call ends and reports VSA_ERR_TIMEOUT.  The normal build then gives
     its results with the workspace zeroed."""
+    if not os.path.exists(vsa_build.NVCC):
+        pytest.skip("needs nvcc")
     b = Batch([1] * 4, [20000] * 4, 8, 8, 64, "bf16")
     good = b.run(False)
     variant = vsa_build.build(lib=str(tmp_path / "libvsa_nowait.so"), defines=("VSA_CACHE_WAIT_NS=0",))
